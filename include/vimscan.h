@@ -563,6 +563,85 @@ size_t vim_scan_ckpt_bytes(int batch, int L, int d_inner, int d_state);
 size_t vmamba_cross_ckpt_bytes(int batch, int H, int W, int channels, int d_state);
 
 /*
+ * ---------------------------------------------------------------------------------
+ * Causal operators: the S6 recurrence and its short convolution in one direction, with
+ * the state handed in and out, for models that read a sequence once from its start
+ * ("Vision Mamba Guide", sections "The Selective State Space (S6) Mechanism" and "2. The
+ * Bidirectional Mamba Block", the forward pathway alone).  They add to the conventions
+ * above:
+ *   - Activations are given by rows (vim_rows), so that a half of one projection's
+ *     output or a few of its columns can be passed as they lie.  Any channel count is
+ *     taken; rows that start on 16-byte boundaries and hold whole 16-byte vectors move
+ *     faster.  Offsets are 64-bit.
+ *   - Sequences (vim_sequences) are the batch rows, or ranges of one packed row.
+ *   - Tables on the device (offsets, slots) are not seen by the host checks.  The kernels
+ *     bound them: no value leads to an access outside the tensors.
+ * ---------------------------------------------------------------------------------
+ */
+
+/* Rows of channels: element (b, t, c) is data[b * batch_stride + t * row_stride + c],
+ * strides in elements. */
+typedef struct {
+    const void *data;
+    int64_t batch_stride, row_stride;
+} vim_rows;
+
+/*
+ * The sequences of a call and their states.
+ *   cu_seqlens : NULL: one sequence per batch row, of L tokens.  Else DEVICE int32
+ *                [n_seqs + 1], non-decreasing: sequence s holds tokens cu_seqlens[s] ..
+ *                cu_seqlens[s+1] - 1 of the single row of L packed tokens (batch = 1);
+ *                empty sequences are allowed.  Tokens before the first and after the last
+ *                sequence belong to none: outputs there are left as they were.
+ *   state      : initial states, one row of n_slots rows per sequence, or NULL (zeros).
+ *   state_out  : receives the final states, or NULL.  May be `state` itself (in place);
+ *                otherwise it must not overlap it, and rows of no sequence stay untouched.
+ *   slots      : DEVICE int32 [n_seqs], the state row of each sequence, or NULL (sequence s
+ *                has row s).  A value outside 0 .. n_slots - 1 marks a padding entry: that
+ *                sequence is skipped, its outputs are left as they were.  Two sequences
+ *                must not name the same row; if they do, that row ends as one of them left
+ *                it (in place, either may have started from the other's result).
+ *   fresh      : DEVICE bytes [n_seqs], or NULL.  Non-zero: the sequence starts from zeros
+ *                whatever its state row holds.
+ */
+typedef struct {
+    const int32_t *cu_seqlens;
+    int n_seqs;
+    const void *state;
+    void *state_out;
+    const int32_t *slots;
+    int n_slots;
+    const unsigned char *fresh;
+} vim_sequences;
+
+/*
+ * Causal selective scan:
+ *   h_t = exp(Delta_t A) h_(t-1) + Delta_t B_t u_t,  Delta_t = softplus(delta_t + delta_bias)
+ *   y_t = (C_t . h_t + D u_t) * silu(z_t)
+ *   u, delta, z, y : rows of d_inner channels (dt); z.data may be NULL (no gate).
+ *   B, C           : rows of d_state (dt), shared by all channels of a token.
+ *   A              : [d_inner, d_state] fp32, any values; D, delta_bias : [d_inner] fp32.
+ *   seqs           : states are fp32 [n_slots, d_inner, d_state], 16-byte aligned.
+ *   ckpt           : NULL, or fp32 causal_ckpt_bytes(batch, L, d_inner, d_state) bytes,
+ *                    16-byte aligned: the state entering every 8th token of a row,
+ *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd.
+ * One launch, no workspace.
+ */
+vim_status causal_scan(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
+                       const float *D, const float *delta_bias, vim_rows y, int batch, int L, int d_inner,
+                       int d_state, vim_dtype dt, const vim_sequences *seqs, float *ckpt, cudaStream_t stream);
+size_t causal_ckpt_bytes(int batch, int L, int d_inner, int d_state);
+
+/*
+ * causal_scan for one token of each of `batch` sequences (seqs->n_seqs = batch, cu_seqlens
+ * ignored): u, delta, z, B, C, y are rows (b, 0) of batch_stride elements each.  state is
+ * required; state_out NULL means in place.
+ */
+vim_status causal_scan_step(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
+                            const float *D, const float *delta_bias, vim_rows y, int batch, int d_inner,
+                            int d_state, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
+
+/*
  * Workspace bytes the scan entry points need (0 when none).  which = 0 for
  * vim_scan_bidir (L_or_H = L, W ignored), 1 for vmamba_cross_scan4 (L_or_H = H).
  * Returns 0 for invalid arguments as well; the entry point then reports them.

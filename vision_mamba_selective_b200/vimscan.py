@@ -719,3 +719,193 @@ def vim_scan_bidir_host(u, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_s
     if st != VIM_OK:
         raise VimScanError(st, "vim_scan_bidir_host")
     return y
+
+
+# ---------------------------------------------------------------------------
+# causal operators
+# ---------------------------------------------------------------------------
+class _Rows(ctypes.Structure):
+    """vim_rows: element (b, t, c) at data[b * batch_stride + t * row_stride + c]."""
+    _fields_ = [("data", _vp), ("batch_stride", _i64), ("row_stride", _i64)]
+
+
+class _Sequences(ctypes.Structure):
+    """vim_sequences."""
+    _fields_ = [("cu_seqlens", _vp), ("n_seqs", _i), ("state", _vp), ("state_out", _vp), ("slots", _vp),
+                ("n_slots", _i), ("fresh", _vp)]
+
+
+_pseq = ctypes.POINTER(_Sequences)
+lib.causal_scan.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp, _Rows, _i, _i, _i, _i, _i, _pseq, _vp, _vp]
+lib.causal_scan.restype = _i
+lib.causal_scan_step.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp, _Rows, _i, _i, _i, _i, _pseq, _vp]
+lib.causal_scan_step.restype = _i
+lib.causal_ckpt_bytes.argtypes = [_i, _i, _i, _i]
+lib.causal_ckpt_bytes.restype = _sz
+_NO_ROWS = _Rows(None, 0, 0)
+
+
+def _check_ref(where, ref):
+    """The device index of the call: that of ``ref``, which must be the current one."""
+    if not isinstance(ref, torch.Tensor) or not ref.is_cuda:
+        raise TypeError(f"{where}: inputs must be CUDA tensors")
+    dev = ref.get_device()
+    cur = torch.cuda.current_device()
+    if dev != cur:
+        raise ValueError(f"{where}: tensors are on {ref.device} but the current device is cuda:{cur}")
+    return dev
+
+
+def _rows(where, name, t, dtype, shape, dev, packed):
+    """vim_rows of activation ``t``: [batch, L, c] (or [L, c] when ``packed``), or [batch, c]
+    for single tokens; any strides with the channels contiguous."""
+    if t is None:
+        return _NO_ROWS
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{where}: {name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{where}: {name} is on {t.device}, the other inputs on cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{where}: the channels of {name} must be contiguous")
+    if len(st) == 3:
+        return _Rows(t.data_ptr(), st[0], st[1])
+    return _Rows(t.data_ptr(), 0, st[0]) if packed else _Rows(t.data_ptr(), st[0], 0)
+
+
+def _sequences(where, ref, n_rows, cu_seqlens, state, state_out, slots, fresh, state_dtype, state_shape):
+    """vim_sequences of a call on ``n_rows`` batch rows, with every table checked."""
+    n = n_rows
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError(f"{where}: cu_seqlens must be a 1-dimensional tensor of n_seqs + 1 offsets")
+        n = cu_seqlens.numel() - 1
+    if state is None and state_out is None:
+        if slots is not None or fresh is not None:
+            raise ValueError(f"{where}: slots and fresh need a state")
+        if cu_seqlens is None:
+            return None, None
+        (pcu,) = _ptrs(where, ref, [("cu_seqlens", cu_seqlens, torch.int32, (n + 1,))])
+        return _Sequences(pcu, n, None, None, None, 0, None), None
+    if state is None and fresh is not None:
+        raise ValueError(f"{where}: fresh needs a state")
+    if state_out is None:
+        state_out = state
+    cache = state_out
+    if cache.dim() != 1 + len(state_shape) or tuple(cache.shape[1:]) != state_shape:
+        raise ValueError(f"{where}: state has shape {tuple(cache.shape)}, expected (slots,) + {state_shape}")
+    if slots is None and cache.shape[0] < n:
+        raise ValueError(f"{where}: state has {cache.shape[0]} rows for {n} sequences")
+    if fresh is not None and fresh.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"{where}: fresh must be bool or uint8, got {fresh.dtype}")
+    pcu, pin, pout, pslots, pfresh = _ptrs(where, ref, [
+        ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)), ("state", state, state_dtype, tuple(cache.shape)),
+        ("state_out", state_out, state_dtype, tuple(cache.shape)), ("slots", slots, torch.int32, (n,)),
+        ("fresh", fresh, None, (n,))])
+    return _Sequences(pcu, n, pin, pout, pslots, cache.shape[0], pfresh), state_out
+
+
+def _launch_stream(stream, *made):
+    """Raw handle of ``stream`` (default: the current one).  Tensors this call allocated
+    belong to the current stream; used on another, they are recorded there, so that the
+    allocator does not hand their memory out while the kernels still use it."""
+    current = torch.cuda.current_stream()
+    if stream is None or stream == current:
+        return current.cuda_stream
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _token_shape(where, x, name, cu_seqlens):
+    """(batch, L, channels) of the activations [batch, L, c], or [L, c] with cu_seqlens."""
+    want = 3 if cu_seqlens is None else 2
+    if x.dim() != want:
+        raise ValueError(f"{where}: {name} must have {want} dimensions "
+                         f"{'[batch, L, channels]' if want == 3 else '[tokens, channels] with cu_seqlens'}, "
+                         f"got {tuple(x.shape)}")
+    return (1, *x.shape) if want == 2 else tuple(x.shape)
+
+
+def causal_ckpt_shape(batch, L, d_inner, d_state):
+    """Shape of the states causal_scan(ckpt=...) keeps and causal_scan_bwd(ckpt=...) takes
+    (batch 1 and L all tokens with cu_seqlens): [batch, ceil(L / 8), d_inner, d_state]."""
+    return (batch, (L + 7) // 8, d_inner, d_state)
+
+
+def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=None, state_out=None, slots=None,
+                fresh=None, ckpt=None, y=None, stream=None):
+    """Causal selective scan; see include/vimscan.h.
+
+    u, delta, z: [batch, L, d_inner], or [tokens, d_inner] with ``cu_seqlens`` (int32,
+    n_seqs + 1 offsets of packed sequences); z may be None.  B, C: the same rows with
+    d_state columns.  Rows may lie apart (a half or some columns of a wider tensor); the
+    channels must be contiguous.  A: [d_inner, d_state], D, delta_bias: [d_inner], fp32.
+
+    state: fp32 [rows, d_inner, d_state]: each sequence starts from its row and leaves its
+    final state there, or in ``state_out`` when that is given (state None and state_out
+    given: start from zeros).  ``slots`` (int32, one per sequence) names the rows, in
+    sequence order by default; a slot outside the cache marks a padding entry, which is
+    skipped.  ``fresh`` (bool, one per sequence) starts a sequence from zeros.
+
+    ``ckpt``, fp32 of causal_ckpt_shape(...), receives the states causal_scan_bwd takes.
+    Returns y, shaped like u.
+    """
+    where = "causal_scan"
+    dev = _check_ref(where, u)
+    batch, L, Di = _token_shape(where, u, "u", cu_seqlens)
+    N = B.shape[-1]
+    packed = cu_seqlens is not None
+    io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
+    made = None
+    if y is None:
+        y = made = torch.empty(act, dtype=io, device=u.device)
+    dt = _dtype_code(u)
+    pA, pD, pbias, pk = _ptrs(where, u, [
+        ("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,)),
+        ("ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N))])
+    seqs, _ = _sequences(where, u, batch, cu_seqlens, state, state_out, slots, fresh, f32, (Di, N))
+    st = lib.causal_scan(
+        _rows(where, "u", u, io, act, dev, packed), _rows(where, "delta", delta, io, act, dev, packed),
+        _rows(where, "z", z, io, act, dev, packed), _rows(where, "B", B, io, bc, dev, packed),
+        _rows(where, "C", C, io, bc, dev, packed), pA, pD, pbias, _rows(where, "y", y, io, act, dev, packed),
+        batch, L, Di, N, dt, seqs, pk, _launch_stream(stream, made))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return y
+
+
+def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=None, slots=None, y=None, stream=None):
+    """causal_scan for one token of each sequence: u, delta, z [batch, d_inner], B, C
+    [batch, d_state], state as there (required; updated in place unless ``state_out`` is
+    given).  Rows whose slot is outside the cache are padding: their y is left as it was.
+    Returns y [batch, d_inner].
+    """
+    where = "causal_scan_step"
+    dev = _check_ref(where, u)
+    if u.dim() != 2:
+        raise ValueError(f"{where}: u must be [batch, d_inner], got {tuple(u.shape)}")
+    if state is None:
+        raise ValueError(f"{where}: a state is needed")
+    batch, Di = u.shape
+    N = B.shape[-1]
+    io, f32, act, bc = u.dtype, torch.float32, u.shape, (batch, N)
+    made = None
+    if y is None:
+        y = made = torch.empty(act, dtype=io, device=u.device)
+    dt = _dtype_code(u)
+    pA, pD, pbias = _ptrs(where, u, [("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,))])
+    seqs, _ = _sequences(where, u, batch, None, state, state_out, slots, None, f32, (Di, N))
+    st = lib.causal_scan_step(
+        _rows(where, "u", u, io, act, dev, False), _rows(where, "delta", delta, io, act, dev, False),
+        _rows(where, "z", z, io, act, dev, False), _rows(where, "B", B, io, bc, dev, False),
+        _rows(where, "C", C, io, bc, dev, False), pA, pD, pbias, _rows(where, "y", y, io, act, dev, False),
+        batch, Di, N, dt, seqs, _launch_stream(stream, made))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return y
