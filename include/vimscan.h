@@ -642,6 +642,29 @@ vim_status causal_scan_step(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, 
                             int d_state, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
 
 /*
+ * Derivative of causal_scan for sequences that start from zeros and whose final states are
+ * not used, for a loss with derivative `dout` with respect to y.
+ *   u, delta, z, B, C, A, D, delta_bias : the forward call's inputs; dout : rows (dt).
+ *   du, ddelta, dz : rows (dt), written; ddelta is with respect to the raw delta; dz.data
+ *               NULL exactly when z.data is.
+ *   dB, dC    : fp32 [batch, L, d_state], contiguous, written.
+ *   dA [d_inner, d_state], dD [d_inner], ddelta_bias [d_inner] : fp32, written.
+ *   cu_seqlens, n_seqs : as in vim_sequences (NULL: one sequence per batch row).  Rows of
+ *               no sequence keep what they held in every output.
+ *   ckpt      : what causal_scan kept for the same inputs, or NULL: formed here.
+ *   workspace : causal_bwd_workspace_bytes(batch, L, d_inner, d_state, ckpt != NULL) bytes,
+ *               256-byte aligned.
+ * Every sum is taken in a fixed order.  No token at all writes zero derivatives of the
+ * parameters.
+ */
+vim_status causal_scan_bwd(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
+                           const float *D, const float *delta_bias, vim_rows dout, vim_rows du, vim_rows ddelta,
+                           vim_rows dz, float *dB, float *dC, float *dA, float *dD, float *ddelta_bias, int batch,
+                           int L, int d_inner, int d_state, vim_dtype dt, const int32_t *cu_seqlens, int n_seqs,
+                           const float *ckpt, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, int has_ckpt);
+
+/*
  * Workspace bytes the scan entry points need (0 when none).  which = 0 for
  * vim_scan_bidir (L_or_H = L, W ignored), 1 for vmamba_cross_scan4 (L_or_H = H).
  * Returns 0 for invalid arguments as well; the entry point then reports them.

@@ -126,9 +126,7 @@ vim_status causal_scan(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_r
     a.state_out = static_cast<float *>(seqs ? seqs->state_out : nullptr);
     a.ckpt = ckpt;
     a.d = d_inner;
-    a.vec_act = whole_vectors(u, dt, batch, L, d_inner) && whole_vectors(delta, dt, batch, L, d_inner) &&
-                whole_vectors(y, dt, batch, L, d_inner) && (!z.data || whole_vectors(z, dt, batch, L, d_inner));
-    a.vec_bc = whole_vectors(B, dt, batch, L, d_state) && whole_vectors(C, dt, batch, L, d_state);
+    a.vec_bc = lane_vectors(B, dt, batch, L, d_state) && lane_vectors(C, dt, batch, L, d_state);
     return launch_pass<kForward>(a, d_state, dt, stream);
 }
 

@@ -16,8 +16,10 @@ namespace vimscan {
 inline bool misaligned(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
 
 // an activation the kernels may address: non-null, aligned to its element, strides >= 0
+// and rows less than 2^29 elements apart
 inline bool bad_rows(const vim_rows &r, vim_dtype dt) {
-    return !r.data || misaligned(r.data, elem_size(dt)) || r.batch_stride < 0 || r.row_stride < 0;
+    return !r.data || misaligned(r.data, elem_size(dt)) || r.batch_stride < 0 || r.row_stride < 0 ||
+           r.row_stride > INT32_MAX / 4;
 }
 // an output: its rows must not overlap (rows of `width` elements)
 inline bool bad_out(const vim_rows &r, vim_dtype dt, int batch, int L, int width) {
@@ -25,13 +27,12 @@ inline bool bad_out(const vim_rows &r, vim_dtype dt, int batch, int L, int width
     if (L > 1 && r.row_stride < width) return true;
     return batch > 1 && r.batch_stride < (int64_t)(L - 1) * r.row_stride + width;
 }
-// whether every row of r starts on a 16-byte boundary and holds whole 16-byte vectors
-inline bool whole_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int width) {
-    const int ve = (int)(16 / elem_size(dt));
-    return !misaligned(r.data, 16) && width % ve == 0 && (L <= 1 || r.row_stride % ve == 0) &&
-           (batch <= 1 || r.batch_stride % ve == 0);
+// whether every row of r (B or C) can be read in vectors of N / 4 elements
+inline bool lane_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int N) {
+    const int n = N >= 4 ? N / 4 : 1;
+    return !misaligned(r.data, n * elem_size(dt)) && (L <= 1 || r.row_stride % n == 0) &&
+           (batch <= 1 || r.batch_stride % n == 0);
 }
-
 inline vim_status check_sizes(int batch, int L, int channels, vim_dtype dt) {
     if (batch < 0 || L < 0 || channels < 0 || (dt != VIM_F32 && dt != VIM_BF16)) return VIM_ERR_INVALID_ARG;
     return VIM_OK;
@@ -109,21 +110,30 @@ __device__ __forceinline__ int sequence_at(const Seqs &q, int t) {
 // ----------------------------------------------------------------------------
 // functions
 // ----------------------------------------------------------------------------
-// exp(x) for x <= 0 to about 1.5e-7 relative at any magnitude: x log2(e) is formed as a
-// rounded product and its remainder, 2^product comes from the exp2 unit and the
-// remainder r enters as 1 + r ln 2.  (Without it the rounding of a product near 10
-// alone is 3e-7 of the result, and softplus at the biases of trained models is exp.)
+// the larger of two, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// exp(x) for x <= 0 to about 1.5e-7 relative: x log2(e) is formed as a rounded product and
+// its remainder r; 2^product comes from the exp2 unit and r enters as 1 + r ln 2.  (Without
+// it the rounding of a product near 10 alone is 3e-7 of the result, and softplus at the
+// biases of trained models is exp.)  Below -100 the result is 0.
 __device__ __forceinline__ float exp_neg(float x) {
+    x = max_nan(x, -100.0f);
     const float t = x * kLog2e;
     const float r = fmaf(x, 1.9259629e-8f, fmaf(x, kLog2e, -t));   // 1.9259629e-8 = log2(e) - float(log2(e))
     const float e = ex2(t);
-    return t < -140.0f ? 0.0f : fmaf(e, r * kLn2, e);
+    return fmaf(e, r * kLn2, e);
 }
 
-// softplus(x) = max(x, 0) + log1p(exp(-|x|)), and x itself above 20: as softplus() of the
-// bidirectional scan, with the exponential above.  There the exponential's error, up to
-// 4e-7 relative, stays below the tolerance of one output; here Delta also scales fp32
-// states that are handed on from call to call and fp32 gradients.
+// softplus(x) = max(x, 0) + log1p(exp(-|x|)): as softplus() of the bidirectional scan, with
+// the exponential above (above 20 the logarithm is below half a step of x, so that x
+// itself comes out).  There the exponential's error, up to 4e-7 relative, stays below the
+// tolerance of one output; here Delta also scales fp32 states that are handed on from
+// call to call and fp32 gradients.
 __device__ __forceinline__ float softplus_acc(float x) {
     const float e = exp_neg(-fabsf(x));
     const float s = e * rcp(2.0f + e);
@@ -134,8 +144,14 @@ __device__ __forceinline__ float softplus_acc(float x) {
     p = fmaf(s2, p, 2.0f / 5.0f);
     p = fmaf(s2, p, 2.0f / 3.0f);
     p = fmaf(s2, p, 2.0f);
-    const float r = fmaf(s, p, fmaxf(x, 0.0f));
-    return x > 20.0f ? x : r;
+    return fmaf(s, p, max_nan(x, 0.0f));
+}
+
+// softplus(x) and its derivative 1 / (1 + exp(-x))
+__device__ __forceinline__ float softplus_slope(float x, float &slope) {
+    const float e = exp_neg(-fabsf(x)), r = rcp(1.0f + e);
+    slope = x < 0.0f ? e * r : r;
+    return softplus_acc(x);
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * kLog2e)); }
@@ -143,5 +159,65 @@ __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * k
 template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// ----------------------------------------------------------------------------
+// elements of strided rows
+// ----------------------------------------------------------------------------
+// an element's bits in a 32-bit register, and its value
+template <typename T> __device__ __forceinline__ float bits_f32(uint32_t v);
+template <> __device__ __forceinline__ float bits_f32<float>(uint32_t v) { return __uint_as_float(v); }
+template <> __device__ __forceinline__ float bits_f32<__nv_bfloat16>(uint32_t v) { return __uint_as_float(v << 16); }
+
+// element i of a run that starts on a word boundary, from its word
+template <typename T> __device__ __forceinline__ float word_f32(uint32_t w, int i) {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+    else return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
+}
+
+// Column `c` of the rows of batch item b.  Row strides fit in 32 bits of bytes (checked on
+// the host), so an address is one widening multiply-add.
+template <typename T>
+struct RowsOf {
+    const char *base;
+    int row;                                               // bytes between rows
+    __device__ __forceinline__ RowsOf(const vim_rows &r, int64_t b, int c)
+        : base(static_cast<const char *>(r.data) + (b * r.batch_stride + c) * (int64_t)sizeof(T)),
+          row((int)(r.row_stride * (int64_t)sizeof(T))) {}
+    __device__ __forceinline__ const char *at(int t) const { return base + (int64_t)t * row; }
+    __device__ __forceinline__ uint32_t raw(int t, int i = 0) const {
+        if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const uint32_t *>(at(t)) + i);
+        else return __ldg(reinterpret_cast<const uint16_t *>(at(t)) + i);
+    }
+    // n 32-bit words of elements: at once, aligned to their size, or element by element
+    template <int n> __device__ __forceinline__ void words(int t, uint32_t (&v)[n]) const {
+        if constexpr (n == 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at(t)));
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+        } else if constexpr (n == 2) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at(t)));
+            v[0] = x.x, v[1] = x.y;
+        } else {
+            v[0] = __ldg(reinterpret_cast<const uint32_t *>(at(t)));
+        }
+    }
+    template <int n> __device__ __forceinline__ void gather(int t, uint32_t (&v)[n]) const {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            if constexpr (sizeof(T) == 4) v[i] = raw(t, i);
+            else v[i] = raw(t, 2 * i) | raw(t, 2 * i + 1) << 16;
+        }
+    }
+    __device__ __forceinline__ void put(int t, float x) const {
+        *reinterpret_cast<T *>(const_cast<char *>(at(t))) = from_f32<T>(x);
+    }
+};
+
+template <int NP> __device__ __forceinline__ void store_row(float *row, const float2 (&v)[NP]) {
+    if constexpr (NP == 2) {
+        *reinterpret_cast<float4 *>(row) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    } else {
+        *reinterpret_cast<float2 *>(row) = v[0];
+    }
+}
 
 }  // namespace vimscan

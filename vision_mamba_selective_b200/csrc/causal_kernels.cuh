@@ -10,24 +10,30 @@
 // What bounds it: A is free per channel and state, so every token-channel takes N
 // exponentials, and the special-function unit gives 16 a clock and SM: with softplus and
 // the gate's sigmoid 20 for N = 16, 1.25 clocks a token-channel, against 0.2 clocks of
-// memory traffic at bf16 and 0.5 of packed FP32 work.  Cutting the sequence into chunks
-// that run side by side costs a second pass over those exponentials (a chunk's end state
-// first, then its outputs), so a sequence is walked once, by one CTA per few channels,
-// and the parallelism comes from the states instead: the N states of a channel are
-// spread over N / NL neighbouring lanes, NL states (1 to 4, in f32x2 pairs) a lane.  The
-// fewer channels there are, the thinner they are spread (see causal_lanes()).
+// memory traffic at bf16 and 0.4 of packed FP32 work.  So no exponential may be computed
+// twice, which rules out the usual two passes over chunks of a sequence (end states
+// first, outputs after), and a walk by one warp per few channels has too few warps: alone
+// on its scheduler a warp issues an instruction every four clocks.
 //
-// A warp handles 32 / LPC channels, LPC = N / NL, in groups of LPC tokens:
-//   - each lane forms Delta and Delta u of ONE token of the group for its channel, a group
-//     ahead, and leaves them in a ring of shared memory that only its warp reads: no
-//     transcendental is computed twice, and no CTA barrier stands in the token loop;
-//   - the recurrence runs token by token on the lane's states, giving LPC partial sums of
-//     C . h, which one reduce-scatter over the channel's lanes turns into the y of the
-//     lane's own token; the same lane gates it and puts it where it had read u.
-// u, delta and z arrive by cp.async in tiles of kTok tokens, two tiles deep; B and C pass
-// through registers, a tile ahead, and stand in shared memory in fp32.  Tiles and groups
-// are aligned to the token axis, and tokens outside the sequence get Delta = 0 and
-// Delta u = 0, which leave the state as it is.
+// The walk is shared by the W warps of a CTA, which all hold the same few channels and
+// take segments of 8 tokens in turn.  For its segment a warp
+//   1. forms Delta and Delta u of its tokens, each lane its share (exchanged by shuffles);
+//   2. runs the segment from h = 0, multiplying up its decays: with P_t the product so far,
+//      h_t = P_t h_in + hz_t, and C_t . h_t = C_t . hz_t + (C_t P_t) . h_in; C_t P_t and the
+//      first sum stay in registers, all of it without knowing h_in;
+//   3. takes h_in from the warp before it and hands h_out on to the next (two multiply-adds
+//      between a named barrier's wait and its arrival: the only serial part), and
+//   4. adds (C_t P_t) . h_in to the sums, two multiply-adds per pair of states and token.
+// A channel's N states lie on N / NL lanes, NL a lane in f32x2 pairs; the partial sums of
+// C . h are reduced over these lanes so that each ends with the y of its own tokens, gates
+// them and stores them.  Lanes of one state group are neighbours: a 16-byte read of B or C
+// then costs two shared-memory clocks, and four if neighbouring lanes read different
+// groups (measured).  Loads run one turn ahead in registers, by single elements, so that
+// any strides and channel counts will do.  Segments are aligned to the token axis; tokens
+// outside the sequence get Delta = 0 and Delta u = 0, which leave the state as it is.
+//
+// The adjoint, and the states kept for the derivative, are wanted only at segment borders:
+// these modes end with step 3.
 #pragma once
 
 #include "causal.cuh"
@@ -45,7 +51,7 @@ struct CausalArgs {
     float *ckpt;                    // [batch][ceil(L / kCkEvery)][d][N] or null
     float *adj;                     // adjoint: carries, [batch][ceil(L / kAdjEvery)][d][N]
     int d;
-    int vec_act, vec_bc;            // rows of u, delta, z, y (B, C) move as 16-byte vectors
+    int vec_bc;                     // B and C can be read by a lane's states at once
 };
 constexpr int kCkEvery = 8;         // tokens between kept states
 constexpr int kAdjEvery = 64;       // tokens between kept adjoint carries
@@ -58,353 +64,238 @@ enum CausalMode {
 
 namespace {
 
-constexpr int kPassThreads = 128;
+constexpr int kSeg = 8;             // tokens per segment
+constexpr int kPassWarps = 8;       // most warps of a CTA: one named barrier each
+static_assert(kCkEvery == kSeg && kAdjEvery % kSeg == 0, "kept states lie at segment borders");
 
-// sums p[0 .. n) over the n neighbouring lanes of a group: lane i of it gets the sum of
-// p[i].  Each step halves the values a lane holds.
-template <int n>
-__device__ __forceinline__ float reduce_scatter(float (&p)[n], int lane) {
+// sums p[0 .. n) over the n lanes of a channel, which are `stride` apart: the i-th of them
+// gets the sum of p[i].  Each step halves the values a lane holds.
+template <int n, int stride>
+__device__ __forceinline__ float reduce_scatter(float (&p)[n], int q) {
 #pragma unroll
     for (int half = n / 2; half >= 1; half >>= 1) {
-        const bool upper = lane & half;
+        const bool upper = q & half;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
             const float send = upper ? p[i] : p[i + half];
             const float keep = upper ? p[i + half] : p[i];
-            p[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+            p[i] = keep + __shfl_xor_sync(0xffffffffu, send, half * stride);
         }
     }
     return p[0];
 }
 
-// shared memory of causal_pass
-template <typename T, int N, int NL, int TOK>
-struct PassStage {
+// one warp's shared memory
+template <int N, int NL>
+struct PassWarp {
     static constexpr int kLanes = N / NL;                  // lanes per channel
-    static constexpr int kCh = kPassThreads / kLanes;      // channels per CTA
-    static constexpr int kRaw = TOK * kCh;                 // elements of one raw tile
-    static constexpr int kBcRow = NL == 1 ? TOK + 4 : N;   // fp32 B/C: [n][tok] or [tok][n]
-    static constexpr int kBc = NL == 1 ? N * kBcRow : TOK * N;
-    // ring rows: kLanes (Delta, Delta u) pairs and 16 bytes, so that the 16-byte reads of a
-    // warp's channels fall into different banks
-    static constexpr int kRingRow = kLanes * 2 + 4;
-    static constexpr int kRing = (kPassThreads / kLanes) * kRingRow;
-    T raw[2][3][kRaw];                                     // u (then y) or dout, delta, z
-    float bc[2][2][kBc];
-    float ring[2][kRing];
+    static constexpr int kCh = 32 / kLanes;                // channels per warp
+    alignas(16) float bc[2][kSeg * N];                     // B and C of its segment
+    alignas(16) float carry[32 * NL];                      // the state handed to it, by lane
 };
 
-template <typename T, int N, int NL, int TOK, int MODE>
-__global__ void __launch_bounds__(kPassThreads) causal_pass(const CausalArgs p) {
-    using S = PassStage<T, N, NL, TOK>;
-    constexpr int LPC = S::kLanes, CH = S::kCh, V = Vec<T>::n;
-    constexpr int NP = NL / 2;                             // f32x2 pairs per lane (NL > 1)
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    S &sm = *reinterpret_cast<S *>(smem_raw);
+__device__ __forceinline__ void named_wait(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void named_arrive(int id) { asm volatile("barrier.arrive %0, 64;" ::"r"(id) : "memory"); }
+
+template <typename T, int N, int NL, int MODE, bool KEEP, bool VEC>
+__global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalArgs p) {
+    using S = PassWarp<N, NL>;
+    constexpr int LPC = S::kLanes, CH = S::kCh, NP = NL / 2;
+    constexpr int EPL = kSeg / LPC;                        // tokens of a segment per lane
+    constexpr int PV = kSeg * N >= 32 ? kSeg * N / 32 : 1; // B (C) values a lane fetches per segment
+    constexpr bool HAS_Z = MODE != kStates, HAS_B = MODE != kAdjoint, HAS_C = MODE != kStates;
+    extern __shared__ __align__(16) unsigned char pass_smem[];
+    const int W = blockDim.x / 32, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    S &sm = reinterpret_cast<S *>(pass_smem)[w];
+    S &next = reinterpret_cast<S *>(pass_smem)[w + 1 == W ? 0 : w + 1];
 
     const int blocks = (p.d + CH - 1) / CH;
     const int s = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * CH;
     const Seq seq = sequence(p.seqs, s);
     const int64_t b = p.seqs.cu ? 0 : s;
-    const int tid = threadIdx.x, q = tid % LPC, cl = tid / LPC, c = c0 + cl;
-    const bool live = c < p.d;
+    const int q = lane / CH, cl = lane % CH;
+    const bool live = c0 + cl < p.d;
+    const int c = live ? c0 + cl : p.d - 1;                // lanes past d repeat the last channel and write nothing
     if (seq.slot < 0) return;                              // a padding entry
 
-    const T *gu = static_cast<const T *>((MODE == kAdjoint ? p.dout : p.u).data) +
-                  b * (MODE == kAdjoint ? p.dout : p.u).batch_stride + c0;
-    const T *gd = static_cast<const T *>(p.delta.data) + b * p.delta.batch_stride + c0;
-    const T *gz = p.z.data ? static_cast<const T *>(p.z.data) + b * p.z.batch_stride + c0 : nullptr;
-    const T *gB = static_cast<const T *>(p.B.data) + b * p.B.batch_stride;
-    const T *gC = static_cast<const T *>(p.C.data) + b * p.C.batch_stride;
-    T *gy = static_cast<T *>(const_cast<void *>(p.y.data)) + b * p.y.batch_stride + c0;
-    const int64_t ru = (MODE == kAdjoint ? p.dout : p.u).row_stride;
+    const vim_rows &urows = MODE == kAdjoint ? p.dout : p.u;
+    const bool gate = p.z.data != nullptr;
+    const RowsOf<T> gu(urows, b, c), gd(p.delta, b, c), gz(gate ? p.z : p.u, b, c), gy(p.y, b, c);
+    const int at = lane * PV;                              // the lane's B (C) values: token, state
+    const RowsOf<T> gB(p.B, b, at % N), gC(p.C, b, at % N);
 
-    // the lane's parameters and state; channels past d run on zeros
-    float A2[NL], h[NL], Dc = 0.0f, bias = 0.0f;
+    float2 A2[NP], h0[NP];
+    load_row<NP>(p.A + (int64_t)c * N + q * NL, A2);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-        A2[i] = live ? p.A[(int64_t)c * N + q * NL + i] * kLog2e : 0.0f;
-        h[i] = 0.0f;
+    for (int i = 0; i < NP; ++i) {
+        A2[i] = mul2(A2[i], f2(kLog2e, kLog2e));
+        h0[i] = f2(0.0f, 0.0f);
     }
-    if (live) {
-        bias = p.bias[c];
-        if (MODE == kForward) Dc = p.D[c];
-        if (p.state && !seq.fresh) {
-            const float *from = p.state + (seq.slot * p.d + c) * N + q * NL;
+    if (p.state && !seq.fresh) load_row<NP>(p.state + (seq.slot * p.d + c) * N + q * NL, h0);
+    const float bias = p.bias[c], Dc = MODE == kForward ? p.D[c] : 0.0f;
+
+    // segments of the sequence; m = 0 is the first in the order of the walk
+    const int first = seq.start / kSeg;
+    const int M = seq.end > seq.start ? (seq.end + kSeg - 1) / kSeg - first : 0;
+    const unsigned length = seq.end - seq.start;
+    auto seg_at = [&](int m) { return (MODE == kAdjoint ? first + M - 1 - m : first + m) * kSeg; };
+
+    // as loaded: anything done to the bits here would wait for the load
+    constexpr int PW = PV == 1 ? 1 : PV * (int)sizeof(T) / 4;
+    uint32_t ru[EPL], rd[EPL], rz[EPL], rb[2][PW];
+    // tokens outside the sequence read its nearest token; what they read is dropped
+    auto nearest = [&](int t) { return min(max(t, seq.start), seq.end - 1); };
+    auto fetch = [&](int m) {
+        const int t0 = seg_at(m);
 #pragma unroll
-            for (int i = 0; i < NL; ++i) h[i] = from[i];
+        for (int e = 0; e < EPL; ++e) {
+            const int t = nearest(t0 + e * LPC + q);
+            ru[e] = gu.raw(t);
+            rd[e] = gd.raw(t);
+            if (HAS_Z) rz[e] = gz.raw(t);
         }
-    }
-
-    const int first = seq.start / TOK;                     // tiles first .. last - 1 of the token axis
-    const int tiles = seq.end > seq.start ? (seq.end + TOK - 1) / TOK - first : 0;
-    auto tile_at = [&](int k) { return (MODE == kAdjoint ? first + tiles - 1 - k : first + k) * TOK; };
-
-    // raw tile k -> buffer k & 1 (rows outside the sequence are not read)
-    auto load_tile = [&](int k) {
-        const int t0 = tile_at(k);
-        T *dst = &sm.raw[k & 1][0][0];
-        if (p.vec_act) {
-            constexpr int PER = CH / V > 0 ? CH / V : 1;   // vectors per row
-#pragma unroll 1
-            for (int i = tid; i < TOK * PER; i += kPassThreads) {
-                const int r = i / PER, j = (i % PER) * V, t = t0 + r;
-                if (t < seq.start || t >= seq.end || c0 + j >= p.d) continue;
-                T *at = dst + r * CH + j;
-                cp_async16(at, gu + t * ru + j, true);
-                cp_async16(at + S::kRaw, gd + t * p.delta.row_stride + j, true);
-                if (gz && MODE != kStates) cp_async16(at + 2 * S::kRaw, gz + t * p.z.row_stride + j, true);
-            }
-            cp_async_commit();
-        } else {
-#pragma unroll 1
-            for (int i = tid; i < TOK * CH; i += kPassThreads) {
-                const int r = i / CH, j = i % CH, t = t0 + r;
-                if (t < seq.start || t >= seq.end || c0 + j >= p.d) continue;
-                dst[i] = gu[t * ru + j];
-                dst[S::kRaw + i] = gd[t * p.delta.row_stride + j];
-                if (gz && MODE != kStates) dst[2 * S::kRaw + i] = gz[t * p.z.row_stride + j];
-            }
+        const int t = nearest(t0 + at / N);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k == 0 ? !HAS_B : !HAS_C) continue;
+            const RowsOf<T> &g = k == 0 ? gB : gC;
+            if (PV == 1) rb[k][0] = g.raw(t);
+            else if (VEC) g.template words<PW>(t, rb[k]);
+            else g.template gather<PW>(t, rb[k]);
         }
     };
 
-    // B (not for the adjoint) and C (not for kept states alone) of a tile, as vectors of V
-    // consecutive (token, state) values in registers; zeros outside the sequence, so that
-    // Delta u = 0 meets no NaN there
-    constexpr bool HAS_B = MODE != kAdjoint, HAS_C = MODE != kStates;
-    constexpr int BCV = TOK * N / V;                       // vectors of one of them
-    constexpr int PF = (BCV + kPassThreads - 1) / kPassThreads;
-    uint4 pre[2][PF];
-    auto load_bc = [&](int k) {
-        const int t0 = tile_at(k);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            if (w == 0 ? !HAS_B : !HAS_C) continue;
-            const T *src = w == 0 ? gB : gC;
-            const int64_t row = w == 0 ? p.B.row_stride : p.C.row_stride;
-#pragma unroll
-            for (int f = 0; f < PF; ++f) {
-                const int v = tid + f * kPassThreads;
-                pre[w][f] = make_uint4(0, 0, 0, 0);
-                if (v >= BCV) continue;
-                if (N % V == 0 && p.vec_bc) {
-                    const int t = t0 + v * V / N;
-                    if (t >= seq.start && t < seq.end)
-                        pre[w][f] = *reinterpret_cast<const uint4 *>(src + t * row + v * V % N);
-                } else {
-                    T e[V];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const int t = t0 + (v * V + i) / N;
-                        e[i] = t >= seq.start && t < seq.end ? src[t * row + (v * V + i) % N] : from_f32<T>(0.0f);
-                    }
-                    pre[w][f] = *reinterpret_cast<const uint4 *>(e);
-                }
-            }
-        }
-    };
-    auto store_bc = [&](int k) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            if (w == 0 ? !HAS_B : !HAS_C) continue;
-#pragma unroll
-            for (int f = 0; f < PF; ++f) {
-                const int v = tid + f * kPassThreads;
-                if (v >= BCV) continue;
-                float e[V];
-                unpack16(pre[w][f], e);
-                float *dst = sm.bc[k & 1][w];
-                if constexpr (NL == 1) {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) dst[((v * V + i) % N) * S::kBcRow + (v * V + i) / N] = e[i];
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; i += 4)
-                        *reinterpret_cast<float4 *>(dst + v * V + i) = make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
-                }
-            }
-        }
-    };
-
-    // rows of y that the last tile left in its raw buffer -> global
-    auto store_tile = [&](int k) {
-        const int t0 = tile_at(k);
-        const T *src = &sm.raw[k & 1][0][0];
-        if (p.vec_act) {
-            constexpr int PER = CH / V > 0 ? CH / V : 1;
+    if (w < M) fetch(w);
 #pragma unroll 1
-            for (int i = tid; i < TOK * PER; i += kPassThreads) {
-                const int r = i / PER, j = (i % PER) * V, t = t0 + r;
-                if (t < seq.start || t >= seq.end || c0 + j >= p.d) continue;
-                *reinterpret_cast<uint4 *>(gy + t * p.y.row_stride + j) = *reinterpret_cast<const uint4 *>(src + r * CH + j);
+    for (int m = w; m < M; m += W) {
+        const int t0 = seg_at(m);
+        // 1. the lane's tokens: (Delta, Delta u), or (Delta, dy) for the adjoint
+        float u_own[EPL], z_own[EPL];
+        float dt_own[EPL], x_own[EPL];
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const int r = e * LPC + q;
+            const float u = bits_f32<T>(ru[e]), z = HAS_Z ? bits_f32<T>(rz[e]) : 0.0f;
+            const float dt = softplus_acc(bits_f32<T>(rd[e]) + bias);
+            const float sg = gate ? z * sigmoid(z) : 1.0f;
+            const bool ok = (unsigned)(t0 + r - seq.start) < length;
+            dt_own[e] = ok ? dt : 0.0f;
+            x_own[e] = ok ? (MODE == kAdjoint ? u * sg : dt * u) : 0.0f;
+            u_own[e] = u;
+            z_own[e] = sg;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k == 0 ? !HAS_B : !HAS_C) continue;
+            // a zero factor outside the sequence, so that Delta u = 0 (dy = 0) meets no NaN there
+            const bool ok = (unsigned)(t0 + at / N - seq.start) < length;
+            float f[PV];
+#pragma unroll
+            for (int i = 0; i < PV; ++i) {
+                const uint32_t word = ok ? rb[k][i * PW / PV] : 0;
+                f[i] = PV == 1 ? bits_f32<T>(word) : word_f32<T>(word, i);
             }
-        } else {
-#pragma unroll 1
-            for (int i = tid; i < TOK * CH; i += kPassThreads) {
-                const int r = i / CH, j = i % CH, t = t0 + r;
-                if (t < seq.start || t >= seq.end || c0 + j >= p.d) continue;
-                gy[t * p.y.row_stride + j] = src[i];
+            if constexpr (PV == 4) {
+                *reinterpret_cast<float4 *>(&sm.bc[k][at]) = make_float4(f[0], f[1], f[2], f[3]);
+            } else if (at < kSeg * N) {
+#pragma unroll
+                for (int i = 0; i < PV; ++i) sm.bc[k][at + i] = f[i];
             }
         }
-    };
+        if (m + W < M) fetch(m + W);
+        __syncwarp();
 
-    constexpr int GROUPS = TOK / LPC;
-    if (tiles > 0) {
-        load_tile(0);
-        load_bc(0);
-        store_bc(0);
-    }
-#pragma unroll 1
-    for (int k = 0; k < tiles; ++k) {
-        cp_async_wait_all();
-        __syncthreads();                                   // tile k is there; tile k - 1 is done with
-        if (MODE == kForward && k > 0) {
-            store_tile(k - 1);
-            __syncthreads();                               // its buffer may be written again
-        }
-        if (k + 1 < tiles) {
-            load_tile(k + 1);
-            load_bc(k + 1);
-        }
-        const int t0 = tile_at(k);
-        T *raw = &sm.raw[k & 1][0][0];
-        const float *Bs = sm.bc[k & 1][0], *Cs = sm.bc[k & 1][1];
-
-        // what the recurrence needs of the lane's own token of group g: (Delta, Delta u), or
-        // (Delta, dy) for the adjoint; returns u
-        auto form = [&](int g) {
-            const int r = g * LPC + q, t = t0 + r;
-            float dt = 0.0f, x = 0.0f, u = 0.0f;
-            if (t >= seq.start && t < seq.end && live) {
-                u = to_f32(raw[r * CH + cl]);
-                dt = softplus_acc(to_f32(raw[S::kRaw + r * CH + cl]) + bias);
+        // 2. the segment from zero, the product of its decays so far, and what y takes of both
+        float2 reach[MODE == kForward ? kSeg : 1][NP], part0[MODE == kForward ? kSeg : 1], P[NP], hz[NP];
+#pragma unroll
+        for (int jj = 0; jj < kSeg; ++jj) {
+            const int j = MODE == kAdjoint ? kSeg - 1 - jj : jj;
+            const float dt = __shfl_sync(0xffffffffu, dt_own[j / LPC], j % LPC * CH + cl);
+            const float x1 = __shfl_sync(0xffffffffu, x_own[j / LPC], j % LPC * CH + cl);
+            float2 rowB[NP], rowC[NP];
+            if (HAS_B) load_row<NP>(&sm.bc[0][j * N + q * NL], rowB);
+            if (HAS_C) load_row<NP>(&sm.bc[1][j * N + q * NL], rowC);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const float2 e = mul2(A2[i], f2(dt, dt));
+                const float2 d = f2(ex2(e.x), ex2(e.y));
+                P[i] = jj == 0 ? d : mul2(P[i], d);
                 if (MODE == kAdjoint) {
-                    x = u;
-                    if (gz) {
-                        const float z = to_f32(raw[2 * S::kRaw + r * CH + cl]);
-                        x = u * (z * sigmoid(z));
-                    }
+                    const float2 x = mul2(rowC[i], f2(x1, x1));
+                    hz[i] = mul2(d, jj == 0 ? x : __fadd2_rn(hz[i], x));
                 } else {
-                    x = dt * u;
+                    const float2 x = mul2(rowB[i], f2(x1, x1));
+                    hz[i] = jj == 0 ? x : fma2(d, hz[i], x);
                 }
-            }
-            *reinterpret_cast<float2 *>(&sm.ring[g & 1][cl * S::kRingRow + 2 * q]) = f2(dt, x);
-            return u;
-        };
-
-        float u_next = form(MODE == kAdjoint ? GROUPS - 1 : 0);
-#pragma unroll 1
-        for (int gi = 0; gi < GROUPS; ++gi) {
-            const int g = MODE == kAdjoint ? GROUPS - 1 - gi : gi;
-            const float u_own = u_next;
-            __syncwarp();
-            const float4 *ring = reinterpret_cast<const float4 *>(&sm.ring[g & 1][cl * S::kRingRow]);
-            float2 v[LPC];
-#pragma unroll
-            for (int i = 0; i < LPC / 2; ++i) {
-                const float4 f = ring[i];
-                v[2 * i] = f2(f.x, f.y);
-                v[2 * i + 1] = f2(f.z, f.w);
-            }
-            if (gi + 1 < GROUPS) u_next = form(MODE == kAdjoint ? g - 1 : g + 1);
-
-            float part[LPC];
-            float Bq[LPC], Cq[LPC];
-            if constexpr (NL == 1) {                       // the lane's state, all tokens of the group
-                constexpr int W = LPC < 4 ? LPC : 4;
-#pragma unroll
-                for (int i = 0; i < LPC; i += W) {
-#pragma unroll
-                    for (int e = 0; e < W; ++e) {
-                        if (HAS_B) Bq[i + e] = Bs[q * S::kBcRow + g * LPC + i + e];
-                        if (HAS_C) Cq[i + e] = Cs[q * S::kBcRow + g * LPC + i + e];
-                    }
+                if (MODE == kForward) {
+                    part0[j] = i == 0 ? mul2(rowC[i], hz[i]) : fma2(rowC[i], hz[i], part0[j]);
+                    reach[j][i] = mul2(rowC[i], P[i]);
                 }
-            }
-#pragma unroll
-            for (int ji = 0; ji < LPC; ++ji) {
-                const int j = MODE == kAdjoint ? LPC - 1 - ji : ji;
-                const int r = g * LPC + j, t = t0 + r;
-                if (MODE != kAdjoint && p.ckpt && (j % kCkEvery) == 0 && (LPC >= kCkEvery || (r % kCkEvery) == 0) &&
-                    t >= seq.start && t < seq.end && live) {
-                    const int64_t row = b * ((p.seqs.L + kCkEvery - 1) / kCkEvery) + t / kCkEvery;
-                    float *to = p.ckpt + (row * p.d + c) * N + q * NL;
-#pragma unroll
-                    for (int i = 0; i < NL; ++i) to[i] = h[i];
-                }
-                const float dt = v[j].x, x = v[j].y;
-                if constexpr (NL == 1) {
-                    const float a = ex2(dt * A2[0]);
-                    if (MODE == kAdjoint) {
-                        h[0] = a * fmaf(Cq[j], x, h[0]);
-                    } else {
-                        h[0] = fmaf(a, h[0], x * Bq[j]);
-                        if (HAS_C) part[j] = h[0] * Cq[j];
-                    }
-                } else {
-                    const float2 *B2 = reinterpret_cast<const float2 *>(Bs + r * N + q * NL);
-                    const float2 *C2 = reinterpret_cast<const float2 *>(Cs + r * N + q * NL);
-                    float2 acc = f2(0.0f, 0.0f);
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const float2 e = mul2(f2(A2[2 * i], A2[2 * i + 1]), f2(dt, dt));
-                        const float2 a = f2(ex2(e.x), ex2(e.y));
-                        float2 hh = f2(h[2 * i], h[2 * i + 1]);
-                        if (MODE == kAdjoint) {
-                            hh = mul2(a, fma2(C2[i], f2(x, x), hh));
-                        } else {
-                            hh = fma2(a, hh, mul2(B2[i], f2(x, x)));
-                            if (HAS_C) acc = i == 0 ? mul2(C2[i], hh) : fma2(C2[i], hh, acc);
-                        }
-                        h[2 * i] = hh.x;
-                        h[2 * i + 1] = hh.y;
-                    }
-                    part[j] = acc.x + acc.y;
-                }
-                if (MODE == kAdjoint && (t % kAdjEvery) == 0 && t > seq.start && t < seq.end && live) {
-                    const int64_t row = b * ((p.seqs.L + kAdjEvery - 1) / kAdjEvery) + t / kAdjEvery - 1;
-                    float *to = p.adj + (row * p.d + c) * N + q * NL;
-#pragma unroll
-                    for (int i = 0; i < NL; ++i) to[i] = h[i];
-                }
-            }
-            if (MODE == kForward) {
-                const float ch = reduce_scatter<LPC>(part, q);
-                const int r = g * LPC + q;
-                float y = fmaf(Dc, u_own, ch);
-                if (gz) {
-                    const float z = to_f32(raw[2 * S::kRaw + r * CH + cl]);
-                    y *= z * sigmoid(z);
-                }
-                raw[r * CH + cl] = from_f32<T>(y);
             }
         }
-        if (k + 1 < tiles) store_bc(k + 1);
-    }
-    if (MODE == kForward) {
-        if (tiles > 0) {
-            __syncthreads();
-            store_tile(tiles - 1);
-        }
-    }
-    if (MODE != kStates && p.state_out && live) {
-        float *to = p.state_out + (seq.slot * p.d + c) * N + q * NL;
+
+        // 3. the state entering the segment, and the one leaving it
+        float2 h[NP], out[NP];
+        if (m == 0) {
 #pragma unroll
-        for (int i = 0; i < NL; ++i) to[i] = h[i];
+            for (int i = 0; i < NP; ++i) h[i] = h0[i];
+        } else {
+            if (W > 1) named_wait(w);
+            load_row<NP>(&sm.carry[lane * NL], h);
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) out[i] = fma2(P[i], h[i], hz[i]);
+        if (m + 1 < M) {
+            store_row<NP>(&next.carry[lane * NL], out);
+            if (W > 1) named_arrive(w + 1 == W ? 0 : w + 1);
+        } else if (MODE != kStates && p.state_out && live) {
+            store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, out);
+        }
+        if (KEEP && MODE != kAdjoint && t0 >= seq.start && live) {
+            const int64_t row = b * ((p.seqs.L + kCkEvery - 1) / kCkEvery) + t0 / kCkEvery;
+            store_row<NP>(p.ckpt + (row * p.d + c) * N + q * NL, h);
+        }
+        if (MODE == kAdjoint && t0 % kAdjEvery == 0 && t0 > seq.start && live) {
+            const int64_t row = b * ((p.seqs.L + kAdjEvery - 1) / kAdjEvery) + t0 / kAdjEvery - 1;
+            store_row<NP>(p.adj + (row * p.d + c) * N + q * NL, out);
+        }
+
+        // 4. the segment from h
+        if (MODE == kForward) {
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) {
+                float part[LPC];
+#pragma unroll
+                for (int l = 0; l < LPC; ++l) {
+                    const int j = e * LPC + l;
+                    float2 acc = part0[j];
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) acc = fma2(reach[j][i], h[i], acc);
+                    part[l] = acc.x + acc.y;
+                }
+                const float y = fmaf(Dc, u_own[e], reduce_scatter<LPC, CH>(part, q)) * z_own[e];
+                const int t = t0 + e * LPC + q;
+                if (live && (unsigned)(t - seq.start) < length) gy.put(t, y);
+            }
+        }
+        __syncwarp();                                      // the warp's shared memory may be written again
     }
+    if (M == 0 && w == 0 && MODE != kStates && p.state_out && live)
+        store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, h0);
 }
 
 }  // namespace
 
-// Lanes a channel's states are spread over (N = 16: 4, 8 or 16, N = 8: 4 or 8), by the
-// number of channels over all sequences.  Spreading wider costs issue slots (sums over
-// more lanes, fewer packed pairs), spreading less leaves schedulers without a warp.
-inline int causal_lanes(int N, int64_t channels) {
-    if (N < 8) return N;
-    if (channels >= 8 * 1184) return 4;
-    if (N == 8 || channels >= 4 * 592) return 8;
-    return 16;
+// Warps per CTA.  Eight keep two CTAs an SM busy; four waste less of a short row when
+// there are channels enough to fill the GPU anyway (64 rows of 197 tokens, 768 channels,
+// N = 16, bf16: 102 us with four, 117 with eight; 8 rows of 4097 tokens, 384 channels: 152
+// and 143).  A row has no work for more warps than it has segments.
+inline int pass_warps(int64_t channels, int L) {
+    const int most = channels >= 16384 && L < 1024 ? 4 : kPassWarps;
+    const int segments = (L + kSeg - 1) / kSeg;
+    return segments >= most ? most : segments < 1 ? 1 : segments;
 }
+
 template <int MODE>
 vim_status launch_pass(const CausalArgs &a, int N, vim_dtype dt, cudaStream_t stream);
 

@@ -8,29 +8,26 @@ namespace vimscan {
 namespace {
 
 template <typename T, int N, int NL, int MODE>
-vim_status launch_pass_v(const CausalArgs &a, cudaStream_t stream) {
-    constexpr int TOK = 32;
-    using S = PassStage<T, N, NL, TOK>;
+vim_status launch_pass_v(const CausalArgs &a, int warps, cudaStream_t stream) {
+    using S = PassWarp<N, NL>;
     const int64_t grid = (int64_t)a.seqs.n * ((a.d + S::kCh - 1) / S::kCh);
     if (grid > INT32_MAX) return VIM_ERR_UNSUPPORTED;
-    auto kernel = causal_pass<T, N, NL, TOK, MODE>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(S)) != cudaSuccess)
-        return VIM_ERR_CUDA;
-    kernel<<<(unsigned)grid, kPassThreads, sizeof(S), stream>>>(a);
+    constexpr bool ALWAYS = MODE != kForward;              // the other modes are there to keep states
+    auto kernel = ALWAYS || a.ckpt ? (a.vec_bc ? causal_pass<T, N, NL, MODE, true, true> : causal_pass<T, N, NL, MODE, true, false>)
+                                   : (a.vec_bc ? causal_pass<T, N, NL, MODE, ALWAYS, true> : causal_pass<T, N, NL, MODE, ALWAYS, false>);
+    static_assert(kPassWarps * sizeof(S) <= 48 * 1024, "no opt-in for shared memory");
+    kernel<<<(unsigned)grid, 32 * warps, warps * sizeof(S), stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? VIM_OK : VIM_ERR_CUDA;
 }
 
 template <typename T, int MODE>
 vim_status launch_pass_t(const CausalArgs &a, int N, cudaStream_t stream) {
-    const int lanes = causal_lanes(N, (int64_t)a.seqs.n * a.d);
+    const int warps = pass_warps((int64_t)a.seqs.n * a.d, a.seqs.L);
     switch (N) {
-        case 2: return launch_pass_v<T, 2, 1, MODE>(a, stream);
-        case 4: return launch_pass_v<T, 4, 1, MODE>(a, stream);
-        case 8: return lanes == 4 ? launch_pass_v<T, 8, 2, MODE>(a, stream) : launch_pass_v<T, 8, 1, MODE>(a, stream);
-        default:
-            return lanes == 4   ? launch_pass_v<T, 16, 4, MODE>(a, stream)
-                   : lanes == 8 ? launch_pass_v<T, 16, 2, MODE>(a, stream)
-                                : launch_pass_v<T, 16, 1, MODE>(a, stream);
+        case 2: return launch_pass_v<T, 2, 2, MODE>(a, warps, stream);
+        case 4: return launch_pass_v<T, 4, 2, MODE>(a, warps, stream);
+        case 8: return launch_pass_v<T, 8, 4, MODE>(a, warps, stream);
+        default: return launch_pass_v<T, 16, 4, MODE>(a, warps, stream);
     }
 }
 

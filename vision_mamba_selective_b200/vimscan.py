@@ -742,6 +742,11 @@ lib.causal_scan_step.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _v
 lib.causal_scan_step.restype = _i
 lib.causal_ckpt_bytes.argtypes = [_i, _i, _i, _i]
 lib.causal_ckpt_bytes.restype = _sz
+lib.causal_scan_bwd.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp, _Rows, _Rows, _Rows, _Rows,
+                                _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]
+lib.causal_scan_bwd.restype = _i
+lib.causal_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
+lib.causal_bwd_workspace_bytes.restype = _sz
 _NO_ROWS = _Rows(None, 0, 0)
 
 
@@ -909,3 +914,59 @@ def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=No
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
+
+
+def causal_bwd_workspace_bytes(batch, L, d_inner, d_state, has_ckpt):
+    return int(lib.causal_bwd_workspace_bytes(batch, L, d_inner, d_state, int(bool(has_ckpt))))
+
+
+def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=None, ckpt=None, workspace=None, out=None,
+                    stream=None):
+    """Derivatives of causal_scan, for sequences that start from zeros and whose final states
+    are not used, and a loss whose derivative with respect to y is ``dout``; see
+    include/vimscan.h.
+
+    Returns a dict: du, ddelta (w.r.t. the raw delta), dz (None without z), shaped like u in
+    its dtype; dB and dC (fp32, contiguous, shaped like B); dA [d_inner, d_state], dD and
+    ddelta_bias [d_inner] (fp32).  ``out`` may hold those tensors from an earlier call to be
+    written again (du, ddelta and dz with any row strides).  Tokens of no sequence keep what
+    the outputs held (zeros when allocated here).  ``ckpt``: the states causal_scan(ckpt=...)
+    kept for the same inputs.
+    """
+    where = "causal_scan_bwd"
+    dev = _check_ref(where, u)
+    batch, L, Di = _token_shape(where, u, "u", cu_seqlens)
+    N = B.shape[-1]
+    packed = cu_seqlens is not None
+    io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
+    made = ()
+    if out is None:
+        fill = torch.zeros if packed else torch.empty
+        acts = lambda: fill(act, dtype=io, device=u.device)
+        f = lambda *shape, of=torch.empty: of(shape, dtype=f32, device=u.device)
+        out = dict(du=acts(), ddelta=acts(), dz=None if z is None else acts(), dB=f(*bc, of=fill), dC=f(*bc, of=fill),
+                   dA=f(Di, N), dD=f(Di), ddelta_bias=f(Di))
+        made = tuple(out.values())
+    elif (z is None) != (out["dz"] is None):
+        raise ValueError(f"{where}: out['dz'] must be given exactly when z is")
+    dt = _dtype_code(u)
+    n = cu_seqlens.numel() - 1 if packed and isinstance(cu_seqlens, torch.Tensor) else 0
+    if packed and (cu_seqlens.dim() != 1 or n < 0):
+        raise ValueError(f"{where}: cu_seqlens must be a 1-dimensional tensor of n_seqs + 1 offsets")
+    pA, pD, pbias, pk, pcu, pdB, pdC, pdA, pdD, pdb = _ptrs(where, u, [
+        ("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,)),
+        ("ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N)), ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)),
+        ("out['dB']", out["dB"], f32, bc), ("out['dC']", out["dC"], f32, bc), ("out['dA']", out["dA"], f32, (Di, N)),
+        ("out['dD']", out["dD"], f32, (Di,)), ("out['ddelta_bias']", out["ddelta_bias"], f32, (Di,))])
+    given = workspace
+    ws, ws_bytes = _workspace(causal_bwd_workspace_bytes(batch, L, Di, N, ckpt is not None), workspace, u.device)
+    r = lambda name, t, shape: _rows(where, name, t, io, shape, dev, packed)
+    st = lib.causal_scan_bwd(
+        r("u", u, act), r("delta", delta, act), r("z", z, act), r("B", B, bc), r("C", C, bc), pA, pD, pbias,
+        r("dout", dout, act), r("out['du']", out["du"], act), r("out['ddelta']", out["ddelta"], act),
+        r("out['dz']", out["dz"], act), pdB, pdC, pdA, pdD, pdb, batch, L, Di, N, dt, pcu, n, pk,
+        None if ws is None else ws.data_ptr(), ws_bytes,
+        _launch_stream(stream, *made, *(() if given is not None else (ws,))))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return out
