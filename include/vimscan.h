@@ -665,6 +665,64 @@ vim_status causal_scan_bwd(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, v
 size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, int has_ckpt);
 
 /*
+ * Short causal depthwise convolution, the front of the causal scan ("1D Conv -> SiLU", here
+ * over the past only):
+ *   pre[b,t,c] = b[c] + sum_k w[c][k] x[b, t - width + 1 + k, c],   k = 0 .. width - 1
+ *   y = silu(pre) where `silu` is non-zero, else pre
+ *   x, y   : rows of `channels` (dt); y must not overlap x.
+ *   w      : [channels, width] fp32, width 2, 3 or 4 (the newest tap last); b : [channels]
+ *            fp32 or NULL.
+ *   seqs   : states are [n_slots, width - 1, channels] (dt), aligned to their elements: the
+ *            last width - 1 inputs of the sequence, oldest first.
+ * Sums are formed in fp32 and rounded once.
+ */
+vim_status causal_conv(vim_rows x, const float *w, const float *b, vim_rows y, int batch, int L, int channels,
+                       int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
+/* causal_conv for one token of each of `batch` sequences, rows as in causal_scan_step; state is
+ * required, state_out NULL means in place. */
+vim_status causal_conv_step(vim_rows x, const float *w, const float *b, vim_rows y, int batch, int channels,
+                            int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
+/*
+ * Derivative of causal_conv for sequences that start from zeros and whose final states are
+ * not used.  dout, dx : rows (dt), dx written; dw [channels, width] and db [channels] (NULL
+ * where b is, or where it is not wanted) : fp32, written.  cu_seqlens, n_seqs as in
+ * causal_scan_bwd; rows of no sequence keep what dx held.  workspace :
+ * causal_conv_bwd_workspace_bytes(batch, L, channels, width) bytes, 256-byte aligned.  Every
+ * sum is taken in a fixed order.
+ */
+vim_status causal_conv_bwd(vim_rows x, const float *w, const float *b, vim_rows dout, vim_rows dx, float *dw,
+                           float *db, int batch, int L, int channels, int width, int silu, vim_dtype dt,
+                           const int32_t *cu_seqlens, int n_seqs, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+size_t causal_conv_bwd_workspace_bytes(int batch, int L, int channels, int width);
+
+/* A gradient tensor: n elements of type dtype (VIM_F32 or VIM_BF16) at data, and where its
+ * clipped values go (out == data: in place). */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t n;
+    int64_t dtype;
+} vim_tensor;
+
+/*
+ * The common norm of `count` gradient tensors, and clipping by it (what a training step does
+ * with everything the derivatives above return):
+ *   norm  = sqrt(sum over all elements of g^2)         -> *norm (DEVICE, one float)
+ *   out_i = g_i * min(1, max_norm / (norm + 1e-6)), rounded once to the tensor's type
+ *   tensors   : HOST array; the tensors are in device memory, aligned to their elements,
+ *               contiguous, empty ones allowed.  An `out` must not overlap any other tensor.
+ *   max_norm  : >= 0; infinity clips nothing and, in place, writes nothing but the norm.
+ *   workspace : clip_grad_norm_workspace_bytes(count) bytes, 256-byte aligned.
+ * A norm that is NaN or infinite clips nothing: `out` gets the gradients as they are, and the
+ * caller sees the norm.  The sum is formed in fp64 in a fixed order.  Two launches for every
+ * 120 tensors.
+ */
+vim_status clip_grad_norm(const vim_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+size_t clip_grad_norm_workspace_bytes(int count);
+
+/*
  * Workspace bytes the scan entry points need (0 when none).  which = 0 for
  * vim_scan_bidir (L_or_H = L, W ignored), 1 for vmamba_cross_scan4 (L_or_H = H).
  * Returns 0 for invalid arguments as well; the entry point then reports them.

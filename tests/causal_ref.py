@@ -40,3 +40,27 @@ def scan(u, delta, z, B, C, A, D, bias, cu=None, starts=None):
     else:
         y = torch.stack([rows.get(t, zero) for t in range(u.shape[0])]) if u.shape[0] else torch.zeros(u.shape, dtype=F64)
     return y, (torch.stack(last) if last else torch.zeros((0,) + A.shape, dtype=F64))
+
+
+def conv(x, w, b, silu=True, cu=None, starts=None):
+    """(y, final states [n_seqs, W - 1, channels]); differentiable."""
+    x, w = x.to(F64), w.to(F64)
+    W = w.shape[1]
+    out, last = torch.zeros_like(x), []
+    rows = {}
+    for s, (row, t0, t1) in enumerate(bounds(x, cu)):
+        seq = x[t0:t1] if row is None else x[row, t0:t1]
+        before = torch.zeros((W - 1, x.shape[-1]), dtype=F64) if starts is None else starts[s].to(F64)
+        ext = torch.cat([before, seq], 0)
+        for t in range(t1 - t0):
+            pre = (ext[t:t + W] * w.t()).sum(0)
+            if b is not None:
+                pre = pre + b.to(F64)
+            rows[(t0 + t) if row is None else (row, t0 + t)] = pre / (1 + torch.exp(-pre)) if silu else pre
+        last.append(ext[ext.shape[0] - (W - 1):])
+    zero = torch.zeros(x.shape[-1], dtype=F64)
+    if cu is None:
+        y = torch.stack([torch.stack([rows[r, t] for t in range(x.shape[1])]) for r in range(x.shape[0])]) if rows else out
+    else:
+        y = torch.stack([rows.get(t, zero) for t in range(x.shape[0])]) if x.shape[0] else out
+    return y, (torch.stack(last) if last else torch.zeros((0, W - 1, x.shape[-1]), dtype=F64))

@@ -1,0 +1,248 @@
+// clip.cu -- the common norm of many gradient tensors, and clipping by it (declared in
+// include/vimscan.h).
+//
+//   norm = sqrt(sum_i |g_i|^2),   out_i = g_i min(1, max_norm / (norm + 1e-6))
+//
+// Bound by memory traffic: one read for the norm, one read and one write for the scaling.
+// The tensors are cut into units of 8192 elements, which the CTAs of a grid of fixed size
+// take in turn, so that a few large tensors and hundreds of small ones load the GPU alike;
+// the table of tensors travels in the launch's parameters, so nothing is copied to the
+// device and the launches can be captured.  Squares are summed in fp32 over 8 elements (a
+// relative error of a few 2^-24) and in fp64 from there on; the CTAs' sums are added in a
+// fixed order, by every CTA of the scaling launch for itself, which saves a launch between
+// the two.  The scaling walks the units backwards: what the norm read last is still in L2.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "causal.cuh"
+
+namespace vimscan {
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kClipCtas = 148 * 6;
+constexpr int kUnit = 8192;                // elements per unit
+constexpr int kPerLaunch = 120;            // tensors per launch: the table stays below 4 KB of parameters
+
+struct ClipTable {
+    const void *in[kPerLaunch];
+    void *out[kPerLaunch];
+    int64_t n[kPerLaunch];
+    int first[kPerLaunch];                 // first unit of each tensor
+    unsigned char bf16[kPerLaunch], vec[kPerLaunch];
+    int count, units;
+};
+
+__device__ __forceinline__ int clip_tensor(const ClipTable &t, int unit) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= unit) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// the sum of n squares in fp32, or where that overflowed or may have lost to underflow, in fp64
+template <int n>
+__device__ __forceinline__ double squares(const float (&f)[n]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) s = fmaf(f[i], f[i], s);
+    if (s > 1.0e-28f && s < 3.0e38f) return s;
+    double d = 0.0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) d = fma((double)f[i], (double)f[i], d);
+    return d;
+}
+
+// the sum of a CTA's values; every thread gets it
+__device__ __forceinline__ double cta_sum(double v, double *sums) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (threadIdx.x % 32 == 0) sums[threadIdx.x / 32] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kClipThreads / 32; ++i) s += sums[i];
+    return s;
+}
+
+// calls f(values, how many of them count, element offset) over a unit's elements, 16 bytes at
+// a time where the tensor's base allows it
+template <typename T, typename F>
+__device__ __forceinline__ void clip_unit(const T *in, int64_t from, int n, bool vec, F f) {
+    constexpr int V = Vec<T>::n;
+    const T *at = in + from;
+    const int whole = vec ? n / V : 0;
+    constexpr int AHEAD = 4;
+    for (int i = threadIdx.x; i < whole; i += AHEAD * kClipThreads) {
+        uint4 q[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+            if (i + j * kClipThreads < whole) q[j] = reinterpret_cast<const uint4 *>(at)[i + j * kClipThreads];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            if (i + j * kClipThreads < whole) {
+                float v[V];
+                unpack16(q[j], v);
+                f(v, (int64_t)(i + j * kClipThreads) * V);
+            }
+        }
+    }
+    for (int i = whole * V + threadIdx.x; i < n; i += kClipThreads) {
+        float v[1] = {to_f32(at[i])};
+        f(v, (int64_t)i);
+    }
+}
+
+__global__ void __launch_bounds__(kClipThreads) clip_squares(const __grid_constant__ ClipTable t, double *part) {
+    __shared__ double sums[kClipThreads / 32];
+    double s = 0.0;
+    auto add = [&](auto &v, int64_t) { s += squares(v); };
+    for (int u = blockIdx.x; u < t.units; u += gridDim.x) {
+        const int k = clip_tensor(t, u);
+        const int64_t from = (int64_t)(u - t.first[k]) * kUnit;
+        const int n = (int)min((int64_t)kUnit, t.n[k] - from);
+        if (t.bf16[k]) clip_unit(static_cast<const __nv_bfloat16 *>(t.in[k]), from, n, t.vec[k], add);
+        else clip_unit(static_cast<const float *>(t.in[k]), from, n, t.vec[k], add);
+    }
+    s = cta_sum(s, sums);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+template <typename T, int n>
+__device__ __forceinline__ void clip_put(T *out, const float (&v)[n], float factor) {
+    float r[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) r[i] = v[i] * factor;
+    if constexpr (n == Vec<T>::n) *reinterpret_cast<uint4 *>(out) = pack16(r);
+    else out[0] = from_f32<T>(r[0]);
+}
+
+__global__ void __launch_bounds__(kClipThreads) clip_scale(const __grid_constant__ ClipTable t, const double *part,
+                                                           int parts, float max_norm, float *norm, int in_place) {
+    __shared__ double sums[kClipThreads / 32];
+    cudaGridDependencySynchronize();
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kClipThreads) s += part[i];
+    const double total = sqrt(cta_sum(s, sums));
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+    // a norm that is not finite clips nothing: the gradients stay as they are
+    const double ratio = (double)max_norm / (total + 1.0e-6);
+    const float factor = total < INFINITY && ratio < 1.0 ? (float)ratio : 1.0f;
+    if (factor == 1.0f && in_place) return;
+    for (int u = t.units - 1 - blockIdx.x; u >= 0; u -= gridDim.x) {
+        const int k = clip_tensor(t, u);
+        if (factor == 1.0f && t.in[k] == t.out[k]) continue;
+        const int64_t from = (int64_t)(u - t.first[k]) * kUnit;
+        const int n = (int)min((int64_t)kUnit, t.n[k] - from);
+        if (t.bf16[k]) {
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(t.out[k]) + from;
+            clip_unit(static_cast<const __nv_bfloat16 *>(t.in[k]), from, n, t.vec[k],
+                      [&](auto &v, int64_t i) { clip_put(out + i, v, factor); });
+        } else {
+            float *out = static_cast<float *>(t.out[k]) + from;
+            clip_unit(static_cast<const float *>(t.in[k]), from, n, t.vec[k],
+                      [&](auto &v, int64_t i) { clip_put(out + i, v, factor); });
+        }
+    }
+}
+
+// a tensor written must not overlap another tensor, nor its own input unless it is that input
+bool clip_overlap(const vim_tensor *t, int count) {
+    struct Range {
+        uintptr_t from, to;
+        bool written;
+    };
+    std::vector<Range> r;
+    r.reserve(2 * (size_t)count);
+    for (int i = 0; i < count; ++i) {
+        const uintptr_t bytes = (uintptr_t)t[i].n * elem_size((vim_dtype)t[i].dtype);
+        if (!bytes) continue;
+        const uintptr_t in = reinterpret_cast<uintptr_t>(t[i].data), out = reinterpret_cast<uintptr_t>(t[i].out);
+        r.push_back({out, out + bytes, true});
+        if (in != out) r.push_back({in, in + bytes, false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
+    uintptr_t end = 0, written_end = 0;    // of all ranges so far, and of the written ones
+    for (const Range &x : r) {
+        if (x.from < written_end || (x.written && x.from < end)) return true;
+        end = std::max(end, x.to);
+        if (x.written) written_end = std::max(written_end, x.to);
+    }
+    return false;
+}
+
+int clip_launches(int count) { return count < 1 ? 1 : (count + kPerLaunch - 1) / kPerLaunch; }
+
+vim_status clip_impl(const vim_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
+                     size_t workspace_bytes, cudaStream_t stream) {
+    if (count < 0 || (count > 0 && !tensors) || !norm || misaligned(norm, 4) || !(max_norm >= 0.0f))
+        return VIM_ERR_INVALID_ARG;
+    bool in_place = true;
+    for (int i = 0; i < count; ++i) {
+        const vim_tensor &t = tensors[i];
+        if (t.n < 0 || (t.dtype != VIM_F32 && t.dtype != VIM_BF16)) return VIM_ERR_INVALID_ARG;
+        if (t.n / kUnit >= INT32_MAX / kPerLaunch) return VIM_ERR_UNSUPPORTED;
+        const size_t el = elem_size((vim_dtype)t.dtype);
+        if (t.n > 0 && (!t.data || !t.out || misaligned(t.data, el) || misaligned(t.out, el))) return VIM_ERR_INVALID_ARG;
+        in_place = in_place && t.data == t.out;
+    }
+    if (clip_overlap(tensors, count)) return VIM_ERR_INVALID_ARG;
+    const int launches = clip_launches(count), parts = launches * kClipCtas;
+    if (!workspace || workspace_bytes < parts * sizeof(double) || misaligned(workspace, kAlign)) return VIM_ERR_WORKSPACE;
+    double *part = static_cast<double *>(workspace);
+    auto table = [&](int launch, ClipTable &t) {
+        std::memset(&t, 0, sizeof(t));
+        for (int i = launch * kPerLaunch; i < count && t.count < kPerLaunch; ++i) {
+            const vim_tensor &x = tensors[i];
+            if (x.n == 0) continue;
+            const int k = t.count++;
+            t.in[k] = x.data, t.out[k] = x.out, t.n[k] = x.n;
+            t.bf16[k] = x.dtype == VIM_BF16;
+            t.vec[k] = !misaligned(x.data, 16) && !misaligned(x.out, 16);
+            t.first[k] = t.units;
+            t.units += (int)((x.n + kUnit - 1) / kUnit);
+            if (i == (launch + 1) * kPerLaunch - 1) break;
+        }
+    };
+    ClipTable t;
+    for (int l = 0; l < launches; ++l) {
+        table(l, t);
+        clip_squares<<<kClipCtas, kClipThreads, 0, stream>>>(t, part + (size_t)l * kClipCtas);
+        if (cudaGetLastError() != cudaSuccess) return VIM_ERR_CUDA;
+    }
+    for (int l = launches - 1; l >= 0; --l) {
+        if (launches > 1) table(l, t);
+        const int ctas = t.units < 1 ? 1 : t.units < kClipCtas ? t.units : kClipCtas;
+        if (launch_dependent(clip_scale, dim3(ctas), dim3(kClipThreads), 0, stream, t, (const double *)part, parts,
+                             max_norm, l == 0 ? norm : (float *)nullptr, (int)in_place) != cudaSuccess)
+            return VIM_ERR_CUDA;
+    }
+    return VIM_OK;
+}
+
+}  // namespace
+}  // namespace vimscan
+
+using namespace vimscan;
+
+extern "C" {
+
+size_t clip_grad_norm_workspace_bytes(int count) {
+    return count < 0 ? 0 : round_up((size_t)clip_launches(count) * kClipCtas * sizeof(double));
+}
+
+vim_status clip_grad_norm(const vim_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+    try {   // the host's own tables may not fit in memory
+        return clip_impl(tensors, count, max_norm, norm, workspace, workspace_bytes, stream);
+    } catch (...) {
+        return VIM_ERR_INVALID_ARG;
+    }
+}
+
+}  // extern "C"

@@ -747,6 +747,18 @@ lib.causal_scan_bwd.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp
 lib.causal_scan_bwd.restype = _i
 lib.causal_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
 lib.causal_bwd_workspace_bytes.restype = _sz
+lib.causal_conv.argtypes = [_Rows, _vp, _vp, _Rows, _i, _i, _i, _i, _i, _i, _pseq, _vp]
+lib.causal_conv.restype = _i
+lib.causal_conv_step.argtypes = [_Rows, _vp, _vp, _Rows, _i, _i, _i, _i, _i, _pseq, _vp]
+lib.causal_conv_step.restype = _i
+lib.causal_conv_bwd.argtypes = [_Rows, _vp, _vp, _Rows, _Rows, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _sz, _vp]
+lib.causal_conv_bwd.restype = _i
+lib.causal_conv_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i]
+lib.causal_conv_bwd_workspace_bytes.restype = _sz
+lib.clip_grad_norm.argtypes = [_vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp]
+lib.clip_grad_norm.restype = _i
+lib.clip_grad_norm_workspace_bytes.argtypes = [_i]
+lib.clip_grad_norm_workspace_bytes.restype = _sz
 _NO_ROWS = _Rows(None, 0, 0)
 
 
@@ -782,13 +794,18 @@ def _rows(where, name, t, dtype, shape, dev, packed):
     return _Rows(t.data_ptr(), 0, st[0]) if packed else _Rows(t.data_ptr(), st[0], 0)
 
 
+def _offsets(where, cu_seqlens):
+    """Number of sequences that ``cu_seqlens`` lists (0 for None)."""
+    if cu_seqlens is None:
+        return 0
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError(f"{where}: cu_seqlens must be a 1-dimensional tensor of n_seqs + 1 offsets")
+    return cu_seqlens.numel() - 1
+
+
 def _sequences(where, ref, n_rows, cu_seqlens, state, state_out, slots, fresh, state_dtype, state_shape):
     """vim_sequences of a call on ``n_rows`` batch rows, with every table checked."""
-    n = n_rows
-    if cu_seqlens is not None:
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-            raise ValueError(f"{where}: cu_seqlens must be a 1-dimensional tensor of n_seqs + 1 offsets")
-        n = cu_seqlens.numel() - 1
+    n = n_rows if cu_seqlens is None else _offsets(where, cu_seqlens)
     if state is None and state_out is None:
         if slots is not None or fresh is not None:
             raise ValueError(f"{where}: slots and fresh need a state")
@@ -950,9 +967,7 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     elif (z is None) != (out["dz"] is None):
         raise ValueError(f"{where}: out['dz'] must be given exactly when z is")
     dt = _dtype_code(u)
-    n = cu_seqlens.numel() - 1 if packed and isinstance(cu_seqlens, torch.Tensor) else 0
-    if packed and (cu_seqlens.dim() != 1 or n < 0):
-        raise ValueError(f"{where}: cu_seqlens must be a 1-dimensional tensor of n_seqs + 1 offsets")
+    n = _offsets(where, cu_seqlens)
     pA, pD, pbias, pk, pcu, pdB, pdC, pdA, pdD, pdb = _ptrs(where, u, [
         ("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,)),
         ("ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N)), ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)),
@@ -970,3 +985,157 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     if st != VIM_OK:
         raise VimScanError(st, where)
     return out
+
+
+def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=None, slots=None, fresh=None, y=None,
+                stream=None):
+    """Short causal depthwise convolution, with SiLU unless ``silu`` is false; see
+    include/vimscan.h.
+
+    x: [batch, L, channels], or [tokens, channels] with ``cu_seqlens``, any row strides.  w:
+    [channels, width] fp32, width 2 to 4, the newest tap last; b: [channels] fp32 or None.
+    state: [rows, width - 1, channels] in x's dtype, the last inputs of each sequence, oldest
+    first; state_out, slots and fresh as in causal_scan.  Returns y, shaped like x.
+    """
+    where = "causal_conv"
+    dev = _check_ref(where, x)
+    batch, L, Ch = _token_shape(where, x, "x", cu_seqlens)
+    W = w.shape[-1]
+    packed = cu_seqlens is not None
+    io, f32, act = x.dtype, torch.float32, x.shape
+    made = None
+    if y is None:
+        y = made = torch.empty(act, dtype=io, device=x.device)
+    dt = _dtype_code(x)
+    pw, pb = _ptrs(where, x, [("w", w, f32, (Ch, W)), ("b", b, f32, (Ch,))])
+    seqs, _ = _sequences(where, x, batch, cu_seqlens, state, state_out, slots, fresh, io, (W - 1, Ch))
+    st = lib.causal_conv(_rows(where, "x", x, io, act, dev, packed), pw, pb, _rows(where, "y", y, io, act, dev, packed),
+                         batch, L, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(stream, made))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return y
+
+
+def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, slots=None, y=None, stream=None):
+    """causal_conv for one token of each sequence: x [batch, channels]; state as there
+    (required; updated in place unless ``state_out`` is given).  Rows whose slot is outside
+    the cache are padding: their y is left as it was.  Returns y [batch, channels].
+    """
+    where = "causal_conv_step"
+    dev = _check_ref(where, x)
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x must be [batch, channels], got {tuple(x.shape)}")
+    if state is None:
+        raise ValueError(f"{where}: a state is needed")
+    batch, Ch = x.shape
+    W = w.shape[-1]
+    io, f32, act = x.dtype, torch.float32, x.shape
+    made = None
+    if y is None:
+        y = made = torch.empty(act, dtype=io, device=x.device)
+    dt = _dtype_code(x)
+    pw, pb = _ptrs(where, x, [("w", w, f32, (Ch, W)), ("b", b, f32, (Ch,))])
+    seqs, _ = _sequences(where, x, batch, None, state, state_out, slots, None, io, (W - 1, Ch))
+    st = lib.causal_conv_step(_rows(where, "x", x, io, act, dev, False), pw, pb, _rows(where, "y", y, io, act, dev, False),
+                              batch, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(stream, made))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return y
+
+
+def causal_conv_bwd_workspace_bytes(batch, L, channels, width):
+    return int(lib.causal_conv_bwd_workspace_bytes(batch, L, channels, width))
+
+
+def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None, out=None, stream=None):
+    """Derivatives of causal_conv, for sequences that start from zeros and whose final states
+    are not used, and a loss whose derivative with respect to y is ``dout``; see
+    include/vimscan.h.
+
+    Returns a dict: dx, shaped like x in its dtype; dw [channels, width] and db [channels]
+    (None without b) in fp32.  ``out`` may hold those tensors from an earlier call (dx with
+    any row strides).  Tokens of no sequence keep what dx held (zeros when allocated here).
+    """
+    where = "causal_conv_bwd"
+    dev = _check_ref(where, x)
+    batch, L, Ch = _token_shape(where, x, "x", cu_seqlens)
+    W = w.shape[-1]
+    packed = cu_seqlens is not None
+    io, f32, act = x.dtype, torch.float32, x.shape
+    made = ()
+    if out is None:
+        out = dict(dx=(torch.zeros if packed else torch.empty)(act, dtype=io, device=x.device),
+                   dw=torch.empty((Ch, W), dtype=f32, device=x.device),
+                   db=None if b is None else torch.empty((Ch,), dtype=f32, device=x.device))
+        made = tuple(out.values())
+    elif (b is None) != (out["db"] is None):
+        raise ValueError(f"{where}: out['db'] must be given exactly when b is")
+    dt = _dtype_code(x)
+    n = _offsets(where, cu_seqlens)
+    pw, pb, pcu, pdw, pdb = _ptrs(where, x, [
+        ("w", w, f32, (Ch, W)), ("b", b, f32, (Ch,)), ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)),
+        ("out['dw']", out["dw"], f32, (Ch, W)), ("out['db']", out["db"], f32, (Ch,))])
+    given = workspace
+    ws, ws_bytes = _workspace(causal_conv_bwd_workspace_bytes(batch, L, Ch, W), workspace, x.device)
+    r = lambda name, t: _rows(where, name, t, io, act, dev, packed)
+    st = lib.causal_conv_bwd(r("x", x), pw, pb, r("dout", dout), r("out['dx']", out["dx"]), pdw, pdb, batch, L, Ch, W,
+                             int(bool(silu)), dt, pcu, n, None if ws is None else ws.data_ptr(), ws_bytes,
+                             _launch_stream(stream, *made, *(() if given is not None else (ws,))))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return out
+
+
+def clip_grad_norm_workspace_bytes(count):
+    return int(lib.clip_grad_norm_workspace_bytes(count))
+
+
+def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
+    """The common norm of many gradients, and clipping by it; see include/vimscan.h.
+
+    ``grads``: contiguous CUDA tensors, fp32 or bf16 in any mixture, as a list or tuple, or a
+    dict of them as the *_bwd functions return (None entries are skipped).  They are scaled
+    in place by min(1, max_norm / (norm + 1e-6)), or into ``out`` (the same kind of
+    collection, the same shapes and dtypes).  A norm that is not finite scales nothing.
+    max_norm may be infinite: then nothing but the norm is computed.  Returns the norm, a
+    float32 tensor of one element on the device (``norm`` if given).
+    """
+    where = "clip_grad_norm"
+    src = [t for t in (grads.values() if isinstance(grads, dict) else grads) if t is not None]
+    dst = src if out is None else [t for t in (out.values() if isinstance(out, dict) else out) if t is not None]
+    if len(dst) != len(src):
+        raise ValueError(f"{where}: {len(src)} gradients and {len(dst)} outputs")
+    max_norm = float(max_norm)
+    if not max_norm >= 0:
+        raise ValueError(f"{where}: max_norm must be >= 0, got {max_norm}")
+    dev = torch.cuda.current_device()
+    table = []
+    for i, (t, o) in enumerate(zip(src, dst)):
+        for name, x in ((f"grads[{i}]", t),) if o is t else ((f"grads[{i}]", t), (f"out[{i}]", o)):
+            if not isinstance(x, torch.Tensor) or not x.is_cuda:
+                raise TypeError(f"{where}: {name} must be a CUDA tensor")
+            if x.get_device() != dev:
+                raise ValueError(f"{where}: {name} is on {x.device} but the current device is cuda:{dev}")
+            if not x.is_contiguous():
+                raise ValueError(f"{where}: {name} must be contiguous")
+        if o.dtype != t.dtype or o.shape != t.shape:
+            raise ValueError(f"{where}: out[{i}] must be {t.dtype} of shape {tuple(t.shape)}, got {o.dtype} of "
+                             f"{tuple(o.shape)}")
+        table += (t.data_ptr(), o.data_ptr(), t.numel(), _dtype_code(t))
+    device = torch.device("cuda", dev)
+    made = []
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=device)
+        made.append(norm)
+    elif not isinstance(norm, torch.Tensor) or norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
+        raise ValueError(f"{where}: norm must be one float32 element on cuda:{dev}")
+    n = len(src)
+    given = workspace
+    ws, ws_bytes = _workspace(clip_grad_norm_workspace_bytes(n), workspace, device)
+    if given is None:
+        made.append(ws)
+    st = lib.clip_grad_norm((_i64 * max(1, len(table)))(*table), n, max_norm, norm.data_ptr(), ws.data_ptr(), ws_bytes,
+                            _launch_stream(stream, *made))
+    if st != VIM_OK:
+        raise VimScanError(st, where)
+    return norm
