@@ -606,11 +606,11 @@ typedef struct {
  */
 typedef struct {
     const int32_t *cu_seqlens;
-    int n_seqs;
+    int64_t n_seqs;
     const void *state;
     void *state_out;
     const int32_t *slots;
-    int n_slots;
+    int64_t n_slots;
     const unsigned char *fresh;
 } vim_sequences;
 
@@ -627,9 +627,12 @@ typedef struct {
  *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd.
  * One launch, no workspace.
  */
-vim_status causal_scan(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
-                       const float *D, const float *delta_bias, vim_rows y, int batch, int L, int d_inner,
-                       int d_state, vim_dtype dt, const vim_sequences *seqs, float *ckpt, cudaStream_t stream);
+typedef struct {
+    vim_rows u, delta, z, B, C, y;
+} vim_scan_io;
+vim_status causal_scan(const vim_scan_io *io, const float *A, const float *D, const float *delta_bias, int batch,
+                       int L, int d_inner, int d_state, vim_dtype dt, const vim_sequences *seqs, float *ckpt,
+                       cudaStream_t stream);
 size_t causal_ckpt_bytes(int batch, int L, int d_inner, int d_state);
 
 /*
@@ -637,9 +640,9 @@ size_t causal_ckpt_bytes(int batch, int L, int d_inner, int d_state);
  * ignored): u, delta, z, B, C, y are rows (b, 0) of batch_stride elements each.  state is
  * required; state_out NULL means in place.
  */
-vim_status causal_scan_step(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
-                            const float *D, const float *delta_bias, vim_rows y, int batch, int d_inner,
-                            int d_state, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
+vim_status causal_scan_step(const vim_scan_io *io, const float *A, const float *D, const float *delta_bias,
+                            int batch, int d_inner, int d_state, vim_dtype dt, const vim_sequences *seqs,
+                            cudaStream_t stream);
 
 /*
  * Derivative of causal_scan for sequences that start from zeros and whose final states are
@@ -657,10 +660,12 @@ vim_status causal_scan_step(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, 
  * Every sum is taken in a fixed order.  No token at all writes zero derivatives of the
  * parameters.
  */
-vim_status causal_scan_bwd(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
-                           const float *D, const float *delta_bias, vim_rows dout, vim_rows du, vim_rows ddelta,
-                           vim_rows dz, float *dB, float *dC, float *dA, float *dD, float *ddelta_bias, int batch,
-                           int L, int d_inner, int d_state, vim_dtype dt, const int32_t *cu_seqlens, int n_seqs,
+typedef struct {
+    vim_rows u, delta, z, B, C, dout, du, ddelta, dz;
+} vim_scan_bwd_io;
+vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const float *D, const float *delta_bias,
+                           float *dB, float *dC, float *dA, float *dD, float *ddelta_bias, int batch, int L,
+                           int d_inner, int d_state, vim_dtype dt, const int32_t *cu_seqlens, int n_seqs,
                            const float *ckpt, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, int has_ckpt);
 
@@ -676,11 +681,14 @@ size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, in
  *            last width - 1 inputs of the sequence, oldest first.
  * Sums are formed in fp32 and rounded once.
  */
-vim_status causal_conv(vim_rows x, const float *w, const float *b, vim_rows y, int batch, int L, int channels,
+typedef struct {
+    vim_rows x, y;
+} vim_conv_io;
+vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, int batch, int L, int channels,
                        int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
 /* causal_conv for one token of each of `batch` sequences, rows as in causal_scan_step; state is
  * required, state_out NULL means in place. */
-vim_status causal_conv_step(vim_rows x, const float *w, const float *b, vim_rows y, int batch, int channels,
+vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *b, int batch, int channels,
                             int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
 /*
  * Derivative of causal_conv for sequences that start from zeros and whose final states are
@@ -690,8 +698,11 @@ vim_status causal_conv_step(vim_rows x, const float *w, const float *b, vim_rows
  * causal_conv_bwd_workspace_bytes(batch, L, channels, width) bytes, 256-byte aligned.  Every
  * sum is taken in a fixed order.
  */
-vim_status causal_conv_bwd(vim_rows x, const float *w, const float *b, vim_rows dout, vim_rows dx, float *dw,
-                           float *db, int batch, int L, int channels, int width, int silu, vim_dtype dt,
+typedef struct {
+    vim_rows x, dout, dx;
+} vim_conv_bwd_io;
+vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const float *b, float *dw, float *db,
+                           int batch, int L, int channels, int width, int silu, vim_dtype dt,
                            const int32_t *cu_seqlens, int n_seqs, void *workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 size_t causal_conv_bwd_workspace_bytes(int batch, int L, int channels, int width);

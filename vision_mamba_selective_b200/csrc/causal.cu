@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kStepThreads) causal_step(const StepArgs p) {
         const float du = dt * u;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            h[i] = fmaf(ex2(dt * (A[i] * kLog2e)), h[i], du * to_f32(Bp[i]));
+            h[i] = fmaf(decay(A[i] * kLog2e, dt), h[i], du * to_f32(Bp[i]));
             part = fmaf(to_f32(Cp[i]), h[i], part);
         }
         float *ho = p.state_out + at;
@@ -102,9 +102,11 @@ size_t causal_ckpt_bytes(int batch, int L, int d_inner, int d_state) {
     return (size_t)batch * ((L + kCkEvery - 1) / kCkEvery) * d_inner * d_state * sizeof(float);
 }
 
-vim_status causal_scan(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
-                       const float *D, const float *delta_bias, vim_rows y, int batch, int L, int d_inner,
-                       int d_state, vim_dtype dt, const vim_sequences *seqs, float *ckpt, cudaStream_t stream) {
+vim_status causal_scan(const vim_scan_io *io, const float *A, const float *D, const float *delta_bias, int batch,
+                       int L, int d_inner, int d_state, vim_dtype dt, const vim_sequences *seqs, float *ckpt,
+                       cudaStream_t stream) {
+    if (!io) return VIM_ERR_INVALID_ARG;
+    const vim_rows &u = io->u, &delta = io->delta, &z = io->z, &B = io->B, &C = io->C, &y = io->y;
     vim_status st = check_sizes(batch, L, d_inner, dt);
     if (st != VIM_OK) return st;
     if (!supported_state(d_state)) return VIM_ERR_UNSUPPORTED;
@@ -130,9 +132,11 @@ vim_status causal_scan(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_r
     return launch_pass<kForward>(a, d_state, dt, stream);
 }
 
-vim_status causal_scan_step(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
-                            const float *D, const float *delta_bias, vim_rows y, int batch, int d_inner,
-                            int d_state, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream) {
+vim_status causal_scan_step(const vim_scan_io *io, const float *A, const float *D, const float *delta_bias,
+                            int batch, int d_inner, int d_state, vim_dtype dt, const vim_sequences *seqs,
+                            cudaStream_t stream) {
+    if (!io) return VIM_ERR_INVALID_ARG;
+    const vim_rows &u = io->u, &delta = io->delta, &z = io->z, &B = io->B, &C = io->C, &y = io->y;
     vim_status st = check_sizes(batch, 1, d_inner, dt);
     if (st != VIM_OK) return st;
     if (!supported_state(d_state)) return VIM_ERR_UNSUPPORTED;

@@ -53,7 +53,7 @@ struct Seqs {
 inline vim_status make_seqs(const vim_sequences *v, int batch, int L, size_t align, Seqs *out) {
     Seqs q = {nullptr, nullptr, nullptr, batch, L, 0};
     if (v) {
-        if (v->n_seqs < 0 || v->n_slots < 0) return VIM_ERR_INVALID_ARG;
+        if (v->n_seqs < 0 || v->n_slots < 0 || v->n_seqs > INT32_MAX || v->n_slots > INT32_MAX) return VIM_ERR_INVALID_ARG;
         if (v->cu_seqlens) {
             if (batch != 1 || misaligned(v->cu_seqlens, 4)) return VIM_ERR_INVALID_ARG;
         } else if (v->n_seqs != batch) {
@@ -65,9 +65,9 @@ inline vim_status make_seqs(const vim_sequences *v, int batch, int L, size_t ali
         if (misaligned(v->state, align) || misaligned(v->state_out, align) || misaligned(v->slots, 4))
             return VIM_ERR_INVALID_ARG;
         q.cu = v->cu_seqlens;
-        q.n = v->n_seqs;
+        q.n = (int)v->n_seqs;
         q.slots = v->slots;
-        q.n_slots = v->n_slots;
+        q.n_slots = (int)v->n_slots;
         q.fresh = v->fresh;
     }
     *out = q;
@@ -159,6 +159,19 @@ __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * k
 template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// 2^(A2 dt), the decay of a state over one step (A2 = A log2(e)).  The exp2 unit's results lie
+// low: by 1.6e-8 to 2.9e-8 relative on average for decays of 0.75 to 0.995, which over a
+// memory of hundreds of steps adds up where unbiased roundings of that size would not.  An
+// argument 2e-8 higher takes the mean error there to between -1.5e-8 and 0 (measured over
+// 10^6 arguments per octave; a step of 0 still gives exactly 1), and the addition is part
+// of the multiplication that forms the argument.
+constexpr float kDecayShift = 2.0e-8f;
+__device__ __forceinline__ float decay(float A2, float dt) { return ex2(fmaf(A2, dt, kDecayShift)); }
+__device__ __forceinline__ float2 decay(float2 A2, float dt) {
+    const float2 e = fma2(A2, f2(dt, dt), f2(kDecayShift, kDecayShift));
+    return f2(ex2(e.x), ex2(e.y));
+}
 
 // ----------------------------------------------------------------------------
 // elements of strided rows

@@ -189,8 +189,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) causal_bwd_main(const Causa
                 const bool reset = PACKED && ((first >> j & 1u) || !(in >> j & 1u));
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const float2 ex = mul2(A2[i], f2(dtj, dtj));
-                    a[j][i] = f2(ex2(ex.x), ex2(ex.y));
+                    a[j][i] = decay(A2[i], dtj);
                     m[j][i] = mul2(a[j][i], h[i]);
                     if (reset) m[j][i] = f2(0.0f, 0.0f);
                     h[i] = fma2(rb[i], f2(xj, xj), m[j][i]);
@@ -376,11 +375,13 @@ size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, in
     return causal_bwd_plan(batch, L, d_inner, d_state, has_ckpt != 0).total;
 }
 
-vim_status causal_scan_bwd(vim_rows u, vim_rows delta, vim_rows z, vim_rows B, vim_rows C, const float *A,
-                           const float *D, const float *delta_bias, vim_rows dout, vim_rows du, vim_rows ddelta,
-                           vim_rows dz, float *dB, float *dC, float *dA, float *dD, float *ddelta_bias, int batch,
-                           int L, int d_inner, int d_state, vim_dtype dt, const int32_t *cu_seqlens, int n_seqs,
+vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const float *D, const float *delta_bias,
+                           float *dB, float *dC, float *dA, float *dD, float *ddelta_bias, int batch, int L,
+                           int d_inner, int d_state, vim_dtype dt, const int32_t *cu_seqlens, int n_seqs,
                            const float *ckpt, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!io) return VIM_ERR_INVALID_ARG;
+    const vim_rows &u = io->u, &delta = io->delta, &z = io->z, &B = io->B, &C = io->C, &dout = io->dout,
+                   &du = io->du, &ddelta = io->ddelta, &dz = io->dz;
     vim_status st = check_sizes(batch, L, d_inner, dt);
     if (st != VIM_OK) return st;
     if (!supported_state(d_state)) return VIM_ERR_UNSUPPORTED;

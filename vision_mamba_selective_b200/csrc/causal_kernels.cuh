@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
             if (HAS_C) load_row<NP>(&sm.bc[1][j * N + q * NL], rowC);
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const float2 e = mul2(A2[i], f2(dt, dt));
-                const float2 d = f2(ex2(e.x), ex2(e.y));
+                const float2 d = decay(A2[i], dt);
                 P[i] = jj == 0 ? d : mul2(P[i], d);
                 if (MODE == kAdjoint) {
                     const float2 x = mul2(rowC[i], f2(x1, x1));

@@ -414,8 +414,10 @@ using namespace vimscan;
 
 extern "C" {
 
-vim_status causal_conv(vim_rows x, const float *w, const float *b, vim_rows y, int batch, int L, int channels,
+vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, int batch, int L, int channels,
                        int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream) {
+    if (!io) return VIM_ERR_INVALID_ARG;
+    const vim_rows &x = io->x, &y = io->y;
     vim_status st = conv_check(batch, L, channels, width, dt, w, b);
     if (st != VIM_OK) return st;
     ConvArgs a;
@@ -436,8 +438,10 @@ vim_status causal_conv(vim_rows x, const float *w, const float *b, vim_rows y, i
                          : conv_width<__nv_bfloat16>(kPrompt, a, width, vec, false, stream);
 }
 
-vim_status causal_conv_step(vim_rows x, const float *w, const float *b, vim_rows y, int batch, int channels,
+vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *b, int batch, int channels,
                             int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream) {
+    if (!io) return VIM_ERR_INVALID_ARG;
+    const vim_rows &x = io->x, &y = io->y;
     vim_status st = conv_check(batch, 1, channels, width, dt, w, b);
     if (st != VIM_OK) return st;
     if (!seqs) return VIM_ERR_INVALID_ARG;
@@ -466,10 +470,12 @@ size_t causal_conv_bwd_workspace_bytes(int batch, int L, int channels, int width
     return round_up((size_t)batch * ((L + run - 1) / run) * channels * (width + 1) * sizeof(float));
 }
 
-vim_status causal_conv_bwd(vim_rows x, const float *w, const float *b, vim_rows dout, vim_rows dx, float *dw,
-                           float *db, int batch, int L, int channels, int width, int silu, vim_dtype dt,
+vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const float *b, float *dw, float *db,
+                           int batch, int L, int channels, int width, int silu, vim_dtype dt,
                            const int32_t *cu_seqlens, int n_seqs, void *workspace, size_t workspace_bytes,
                            cudaStream_t stream) {
+    if (!io) return VIM_ERR_INVALID_ARG;
+    const vim_rows &x = io->x, &dout = io->dout, &dx = io->dx;
     vim_status st = conv_check(batch, L, channels, width, dt, w, b);
     if (st != VIM_OK) return st;
     vim_sequences seqs;

@@ -724,34 +724,21 @@ def vim_scan_bidir_host(u, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_s
 # ---------------------------------------------------------------------------
 # causal operators
 # ---------------------------------------------------------------------------
-class _Rows(ctypes.Structure):
-    """vim_rows: element (b, t, c) at data[b * batch_stride + t * row_stride + c]."""
-    _fields_ = [("data", _vp), ("batch_stride", _i64), ("row_stride", _i64)]
-
-
-class _Sequences(ctypes.Structure):
-    """vim_sequences."""
-    _fields_ = [("cu_seqlens", _vp), ("n_seqs", _i), ("state", _vp), ("state_out", _vp), ("slots", _vp),
-                ("n_slots", _i), ("fresh", _vp)]
-
-
-_pseq = ctypes.POINTER(_Sequences)
-lib.causal_scan.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp, _Rows, _i, _i, _i, _i, _i, _pseq, _vp, _vp]
+lib.causal_scan.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]
 lib.causal_scan.restype = _i
-lib.causal_scan_step.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp, _Rows, _i, _i, _i, _i, _pseq, _vp]
+lib.causal_scan_step.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]
 lib.causal_scan_step.restype = _i
 lib.causal_ckpt_bytes.argtypes = [_i, _i, _i, _i]
 lib.causal_ckpt_bytes.restype = _sz
-lib.causal_scan_bwd.argtypes = [_Rows, _Rows, _Rows, _Rows, _Rows, _vp, _vp, _vp, _Rows, _Rows, _Rows, _Rows,
-                                _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]
+lib.causal_scan_bwd.argtypes = [_vp] * 9 + [_i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _sz, _vp]
 lib.causal_scan_bwd.restype = _i
 lib.causal_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i, _i]
 lib.causal_bwd_workspace_bytes.restype = _sz
-lib.causal_conv.argtypes = [_Rows, _vp, _vp, _Rows, _i, _i, _i, _i, _i, _i, _pseq, _vp]
+lib.causal_conv.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp]
 lib.causal_conv.restype = _i
-lib.causal_conv_step.argtypes = [_Rows, _vp, _vp, _Rows, _i, _i, _i, _i, _i, _pseq, _vp]
+lib.causal_conv_step.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp]
 lib.causal_conv_step.restype = _i
-lib.causal_conv_bwd.argtypes = [_Rows, _vp, _vp, _Rows, _Rows, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _sz, _vp]
+lib.causal_conv_bwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _vp, _sz, _vp]
 lib.causal_conv_bwd.restype = _i
 lib.causal_conv_bwd_workspace_bytes.argtypes = [_i, _i, _i, _i]
 lib.causal_conv_bwd_workspace_bytes.restype = _sz
@@ -759,7 +746,10 @@ lib.clip_grad_norm.argtypes = [_vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp]
 lib.clip_grad_norm.restype = _i
 lib.clip_grad_norm_workspace_bytes.argtypes = [_i]
 lib.clip_grad_norm_workspace_bytes.restype = _sz
-_NO_ROWS = _Rows(None, 0, 0)
+
+# The structs of the causal entry points (vim_scan_io and the like, vim_sequences, vim_tensor)
+# hold nothing but 64-bit values, so they are handed over as arrays of those.
+_i64x = {n: _i64 * n for n in (6, 7, 9, 18, 27)}
 
 
 def _check_ref(where, ref):
@@ -773,25 +763,40 @@ def _check_ref(where, ref):
     return dev
 
 
-def _rows(where, name, t, dtype, shape, dev, packed):
-    """vim_rows of activation ``t``: [batch, L, c] (or [L, c] when ``packed``), or [batch, c]
-    for single tokens; any strides with the channels contiguous."""
-    if t is None:
-        return _NO_ROWS
+def _on_device(where, name, t, dtype, shape, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{where}: {name} must be a CUDA tensor")
     if t.get_device() != dev:
         raise ValueError(f"{where}: {name} is on {t.device}, the other inputs on cuda:{dev}")
     if t.dtype != dtype:
         raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(where, name, t, dtype, shape, dev, packed):
+    """vim_rows of activation ``t``: [batch, L, c] (or [L, c] when ``packed``), or [batch, c]
+    for single tokens; any strides with the channels contiguous."""
+    if t is None:
+        return 0, 0, 0
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _on_device(where, name, t, dtype, shape, dev)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{where}: the channels of {name} must be contiguous")
     if len(st) == 3:
-        return _Rows(t.data_ptr(), st[0], st[1])
-    return _Rows(t.data_ptr(), 0, st[0]) if packed else _Rows(t.data_ptr(), st[0], 0)
+        return t.data_ptr(), st[0], st[1]
+    return (t.data_ptr(), 0, st[0]) if packed else (t.data_ptr(), st[0], 0)
+
+
+def _table(where, name, t, dtype, shape, dev):
+    """Address of contiguous tensor ``t`` (None for None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _on_device(where, name, t, dtype, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    return t.data_ptr()
 
 
 def _offsets(where, cu_seqlens):
@@ -803,44 +808,42 @@ def _offsets(where, cu_seqlens):
     return cu_seqlens.numel() - 1
 
 
-def _sequences(where, ref, n_rows, cu_seqlens, state, state_out, slots, fresh, state_dtype, state_shape):
+def _sequences(where, dev, n_rows, cu_seqlens, state, state_out, slots, fresh, state_dtype, state_shape):
     """vim_sequences of a call on ``n_rows`` batch rows, with every table checked."""
     n = n_rows if cu_seqlens is None else _offsets(where, cu_seqlens)
+    pcu = _table(where, "cu_seqlens", cu_seqlens, torch.int32, (n + 1,), dev)
     if state is None and state_out is None:
         if slots is not None or fresh is not None:
             raise ValueError(f"{where}: slots and fresh need a state")
-        if cu_seqlens is None:
-            return None, None
-        (pcu,) = _ptrs(where, ref, [("cu_seqlens", cu_seqlens, torch.int32, (n + 1,))])
-        return _Sequences(pcu, n, None, None, None, 0, None), None
+        return None if pcu is None else _i64x[7](pcu, n, 0, 0, 0, 0, 0)
     if state is None and fresh is not None:
         raise ValueError(f"{where}: fresh needs a state")
     if state_out is None:
         state_out = state
-    cache = state_out
-    if cache.dim() != 1 + len(state_shape) or tuple(cache.shape[1:]) != state_shape:
-        raise ValueError(f"{where}: state has shape {tuple(cache.shape)}, expected (slots,) + {state_shape}")
-    if slots is None and cache.shape[0] < n:
-        raise ValueError(f"{where}: state has {cache.shape[0]} rows for {n} sequences")
+    if state_out.dim() != 1 + len(state_shape) or tuple(state_out.shape[1:]) != state_shape:
+        raise ValueError(f"{where}: state has shape {tuple(state_out.shape)}, expected (slots,) + {state_shape}")
+    shape = state_out.shape
+    if slots is None and shape[0] < n:
+        raise ValueError(f"{where}: state has {shape[0]} rows for {n} sequences")
     if fresh is not None and fresh.dtype not in (torch.bool, torch.uint8):
         raise TypeError(f"{where}: fresh must be bool or uint8, got {fresh.dtype}")
-    pcu, pin, pout, pslots, pfresh = _ptrs(where, ref, [
-        ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)), ("state", state, state_dtype, tuple(cache.shape)),
-        ("state_out", state_out, state_dtype, tuple(cache.shape)), ("slots", slots, torch.int32, (n,)),
-        ("fresh", fresh, None, (n,))])
-    return _Sequences(pcu, n, pin, pout, pslots, cache.shape[0], pfresh), state_out
+    pout = _table(where, "state_out", state_out, state_dtype, shape, dev)
+    pin = pout if state is state_out else _table(where, "state", state, state_dtype, shape, dev)
+    pslots = _table(where, "slots", slots, torch.int32, (n,), dev)
+    pfresh = None if fresh is None else _table(where, "fresh", fresh, fresh.dtype, (n,), dev)
+    return _i64x[7](pcu or 0, n, pin or 0, pout, pslots or 0, shape[0], pfresh or 0)
 
 
-def _launch_stream(stream, *made):
+def _launch_stream(dev, stream, *made):
     """Raw handle of ``stream`` (default: the current one).  Tensors this call allocated
     belong to the current stream; used on another, they are recorded there, so that the
     allocator does not hand their memory out while the kernels still use it."""
-    current = torch.cuda.current_stream()
-    if stream is None or stream == current:
-        return current.cuda_stream
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -884,19 +887,19 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
     N = B.shape[-1]
     packed = cu_seqlens is not None
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
+    dt = _dtype_code(u)
     made = None
     if y is None:
         y = made = torch.empty(act, dtype=io, device=u.device)
-    dt = _dtype_code(u)
-    pA, pD, pbias, pk = _ptrs(where, u, [
-        ("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,)),
-        ("ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N))])
-    seqs, _ = _sequences(where, u, batch, cu_seqlens, state, state_out, slots, fresh, f32, (Di, N))
-    st = lib.causal_scan(
-        _rows(where, "u", u, io, act, dev, packed), _rows(where, "delta", delta, io, act, dev, packed),
-        _rows(where, "z", z, io, act, dev, packed), _rows(where, "B", B, io, bc, dev, packed),
-        _rows(where, "C", C, io, bc, dev, packed), pA, pD, pbias, _rows(where, "y", y, io, act, dev, packed),
-        batch, L, Di, N, dt, seqs, pk, _launch_stream(stream, made))
+    rows = _i64x[18](
+        *_rows(where, "u", u, io, act, dev, packed), *_rows(where, "delta", delta, io, act, dev, packed),
+        *_rows(where, "z", z, io, act, dev, packed), *_rows(where, "B", B, io, bc, dev, packed),
+        *_rows(where, "C", C, io, bc, dev, packed), *_rows(where, "y", y, io, act, dev, packed))
+    pA, pD = _table(where, "A", A, f32, (Di, N), dev), _table(where, "D", D, f32, (Di,), dev)
+    pbias = _table(where, "delta_bias", delta_bias, f32, (Di,), dev)
+    pk = None if ckpt is None else _table(where, "ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N), dev)
+    seqs = _sequences(where, dev, batch, cu_seqlens, state, state_out, slots, fresh, f32, (Di, N))
+    st = lib.causal_scan(rows, pA, pD, pbias, batch, L, Di, N, dt, seqs, pk, _launch_stream(dev, stream, made))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
@@ -917,17 +920,18 @@ def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=No
     batch, Di = u.shape
     N = B.shape[-1]
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (batch, N)
+    dt = _dtype_code(u)
     made = None
     if y is None:
         y = made = torch.empty(act, dtype=io, device=u.device)
-    dt = _dtype_code(u)
-    pA, pD, pbias = _ptrs(where, u, [("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,))])
-    seqs, _ = _sequences(where, u, batch, None, state, state_out, slots, None, f32, (Di, N))
-    st = lib.causal_scan_step(
-        _rows(where, "u", u, io, act, dev, False), _rows(where, "delta", delta, io, act, dev, False),
-        _rows(where, "z", z, io, act, dev, False), _rows(where, "B", B, io, bc, dev, False),
-        _rows(where, "C", C, io, bc, dev, False), pA, pD, pbias, _rows(where, "y", y, io, act, dev, False),
-        batch, Di, N, dt, seqs, _launch_stream(stream, made))
+    rows = _i64x[18](
+        *_rows(where, "u", u, io, act, dev, False), *_rows(where, "delta", delta, io, act, dev, False),
+        *_rows(where, "z", z, io, act, dev, False), *_rows(where, "B", B, io, bc, dev, False),
+        *_rows(where, "C", C, io, bc, dev, False), *_rows(where, "y", y, io, act, dev, False))
+    pA, pD = _table(where, "A", A, f32, (Di, N), dev), _table(where, "D", D, f32, (Di,), dev)
+    pbias = _table(where, "delta_bias", delta_bias, f32, (Di,), dev)
+    seqs = _sequences(where, dev, batch, None, state, state_out, slots, None, f32, (Di, N))
+    st = lib.causal_scan_step(rows, pA, pD, pbias, batch, Di, N, dt, seqs, _launch_stream(dev, stream, made))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
@@ -968,20 +972,23 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
         raise ValueError(f"{where}: out['dz'] must be given exactly when z is")
     dt = _dtype_code(u)
     n = _offsets(where, cu_seqlens)
-    pA, pD, pbias, pk, pcu, pdB, pdC, pdA, pdD, pdb = _ptrs(where, u, [
-        ("A", A, f32, (Di, N)), ("D", D, f32, (Di,)), ("delta_bias", delta_bias, f32, (Di,)),
-        ("ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N)), ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)),
-        ("out['dB']", out["dB"], f32, bc), ("out['dC']", out["dC"], f32, bc), ("out['dA']", out["dA"], f32, (Di, N)),
-        ("out['dD']", out["dD"], f32, (Di,)), ("out['ddelta_bias']", out["ddelta_bias"], f32, (Di,))])
+    tab = lambda name, t, shape, dtype=f32: _table(where, name, t, dtype, shape, dev)
+    pA, pD, pbias = tab("A", A, (Di, N)), tab("D", D, (Di,)), tab("delta_bias", delta_bias, (Di,))
+    pk = None if ckpt is None else tab("ckpt", ckpt, causal_ckpt_shape(batch, L, Di, N))
+    pcu = tab("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
+    pdB, pdC = tab("out['dB']", out["dB"], bc), tab("out['dC']", out["dC"], bc)
+    pdA, pdD = tab("out['dA']", out["dA"], (Di, N)), tab("out['dD']", out["dD"], (Di,))
+    pdb = tab("out['ddelta_bias']", out["ddelta_bias"], (Di,))
+    r = lambda name, t, shape: _rows(where, name, t, io, shape, dev, packed)
+    rows = _i64x[27](
+        *r("u", u, act), *r("delta", delta, act), *r("z", z, act), *r("B", B, bc), *r("C", C, bc), *r("dout", dout, act),
+        *r("out['du']", out["du"], act), *r("out['ddelta']", out["ddelta"], act), *r("out['dz']", out["dz"], act))
     given = workspace
     ws, ws_bytes = _workspace(causal_bwd_workspace_bytes(batch, L, Di, N, ckpt is not None), workspace, u.device)
-    r = lambda name, t, shape: _rows(where, name, t, io, shape, dev, packed)
     st = lib.causal_scan_bwd(
-        r("u", u, act), r("delta", delta, act), r("z", z, act), r("B", B, bc), r("C", C, bc), pA, pD, pbias,
-        r("dout", dout, act), r("out['du']", out["du"], act), r("out['ddelta']", out["ddelta"], act),
-        r("out['dz']", out["dz"], act), pdB, pdC, pdA, pdD, pdb, batch, L, Di, N, dt, pcu, n, pk,
+        rows, pA, pD, pbias, pdB, pdC, pdA, pdD, pdb, batch, L, Di, N, dt, pcu, n, pk,
         None if ws is None else ws.data_ptr(), ws_bytes,
-        _launch_stream(stream, *made, *(() if given is not None else (ws,))))
+        _launch_stream(dev, stream, *made, *(() if given is not None else (ws,))))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return out
@@ -1007,10 +1014,10 @@ def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=No
     if y is None:
         y = made = torch.empty(act, dtype=io, device=x.device)
     dt = _dtype_code(x)
-    pw, pb = _ptrs(where, x, [("w", w, f32, (Ch, W)), ("b", b, f32, (Ch,))])
-    seqs, _ = _sequences(where, x, batch, cu_seqlens, state, state_out, slots, fresh, io, (W - 1, Ch))
-    st = lib.causal_conv(_rows(where, "x", x, io, act, dev, packed), pw, pb, _rows(where, "y", y, io, act, dev, packed),
-                         batch, L, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(stream, made))
+    rows = _i64x[6](*_rows(where, "x", x, io, act, dev, packed), *_rows(where, "y", y, io, act, dev, packed))
+    pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
+    seqs = _sequences(where, dev, batch, cu_seqlens, state, state_out, slots, fresh, io, (W - 1, Ch))
+    st = lib.causal_conv(rows, pw, pb, batch, L, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(dev, stream, made))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
@@ -1034,10 +1041,10 @@ def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, slots=None, y
     if y is None:
         y = made = torch.empty(act, dtype=io, device=x.device)
     dt = _dtype_code(x)
-    pw, pb = _ptrs(where, x, [("w", w, f32, (Ch, W)), ("b", b, f32, (Ch,))])
-    seqs, _ = _sequences(where, x, batch, None, state, state_out, slots, None, io, (W - 1, Ch))
-    st = lib.causal_conv_step(_rows(where, "x", x, io, act, dev, False), pw, pb, _rows(where, "y", y, io, act, dev, False),
-                              batch, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(stream, made))
+    rows = _i64x[6](*_rows(where, "x", x, io, act, dev, False), *_rows(where, "y", y, io, act, dev, False))
+    pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
+    seqs = _sequences(where, dev, batch, None, state, state_out, slots, None, io, (W - 1, Ch))
+    st = lib.causal_conv_step(rows, pw, pb, batch, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(dev, stream, made))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
@@ -1072,15 +1079,16 @@ def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None
         raise ValueError(f"{where}: out['db'] must be given exactly when b is")
     dt = _dtype_code(x)
     n = _offsets(where, cu_seqlens)
-    pw, pb, pcu, pdw, pdb = _ptrs(where, x, [
-        ("w", w, f32, (Ch, W)), ("b", b, f32, (Ch,)), ("cu_seqlens", cu_seqlens, torch.int32, (n + 1,)),
-        ("out['dw']", out["dw"], f32, (Ch, W)), ("out['db']", out["db"], f32, (Ch,))])
+    tab = lambda name, t, shape, dtype=f32: _table(where, name, t, dtype, shape, dev)
+    pw, pb, pcu = tab("w", w, (Ch, W)), tab("b", b, (Ch,)), tab("cu_seqlens", cu_seqlens, (n + 1,), torch.int32)
+    pdw, pdb = tab("out['dw']", out["dw"], (Ch, W)), tab("out['db']", out["db"], (Ch,))
+    r = lambda name, t: _rows(where, name, t, io, act, dev, packed)
+    rows = _i64x[9](*r("x", x), *r("dout", dout), *r("out['dx']", out["dx"]))
     given = workspace
     ws, ws_bytes = _workspace(causal_conv_bwd_workspace_bytes(batch, L, Ch, W), workspace, x.device)
-    r = lambda name, t: _rows(where, name, t, io, act, dev, packed)
-    st = lib.causal_conv_bwd(r("x", x), pw, pb, r("dout", dout), r("out['dx']", out["dx"]), pdw, pdb, batch, L, Ch, W,
-                             int(bool(silu)), dt, pcu, n, None if ws is None else ws.data_ptr(), ws_bytes,
-                             _launch_stream(stream, *made, *(() if given is not None else (ws,))))
+    st = lib.causal_conv_bwd(rows, pw, pb, pdw, pdb, batch, L, Ch, W, int(bool(silu)), dt, pcu, n,
+                             None if ws is None else ws.data_ptr(), ws_bytes,
+                             _launch_stream(dev, stream, *made, *(() if given is not None else (ws,))))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return out
@@ -1088,6 +1096,20 @@ def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None
 
 def clip_grad_norm_workspace_bytes(count):
     return int(lib.clip_grad_norm_workspace_bytes(count))
+
+
+_CLIP_TYPES = {torch.float32: VIM_F32, torch.bfloat16: VIM_BF16}
+
+
+def _refuse_gradient(where, name, t, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{where}: {name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{where}: {name} is on {t.device} but the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous")
+    if t.dtype not in _CLIP_TYPES:
+        raise TypeError(f"{where}: {name}: unsupported dtype {t.dtype}: fp32 or bf16")
 
 
 def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
@@ -1111,17 +1133,17 @@ def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stre
     dev = torch.cuda.current_device()
     table = []
     for i, (t, o) in enumerate(zip(src, dst)):
-        for name, x in ((f"grads[{i}]", t),) if o is t else ((f"grads[{i}]", t), (f"out[{i}]", o)):
-            if not isinstance(x, torch.Tensor) or not x.is_cuda:
-                raise TypeError(f"{where}: {name} must be a CUDA tensor")
-            if x.get_device() != dev:
-                raise ValueError(f"{where}: {name} is on {x.device} but the current device is cuda:{dev}")
-            if not x.is_contiguous():
-                raise ValueError(f"{where}: {name} must be contiguous")
-        if o.dtype != t.dtype or o.shape != t.shape:
+        # one pass of cheap checks; what is wrong is worked out only where one fails
+        if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()
+                and t.dtype in _CLIP_TYPES):
+            _refuse_gradient(where, f"grads[{i}]", t, dev)
+        if o is not t and not (isinstance(o, torch.Tensor) and o.get_device() == dev and o.is_contiguous()
+                               and o.dtype == t.dtype and o.shape == t.shape):
+            _refuse_gradient(where, f"out[{i}]", o, dev)
             raise ValueError(f"{where}: out[{i}] must be {t.dtype} of shape {tuple(t.shape)}, got {o.dtype} of "
                              f"{tuple(o.shape)}")
-        table += (t.data_ptr(), o.data_ptr(), t.numel(), _dtype_code(t))
+        at = t.data_ptr()
+        table += (at, at if o is t else o.data_ptr(), t.numel(), _CLIP_TYPES[t.dtype])
     device = torch.device("cuda", dev)
     made = []
     if norm is None:
@@ -1135,7 +1157,7 @@ def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stre
     if given is None:
         made.append(ws)
     st = lib.clip_grad_norm((_i64 * max(1, len(table)))(*table), n, max_norm, norm.data_ptr(), ws.data_ptr(), ws_bytes,
-                            _launch_stream(stream, *made))
+                            _launch_stream(dev, stream, *made))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return norm
