@@ -19,9 +19,10 @@ struct ConvArgs {
     Seqs seqs;
     const void *state;                     // [n_slots][W - 1][d] or null
     void *state_out;
-    float *part;                           // derivative: [runs][d][W + 1]
+    float *part;                           // derivative: [groups of runs][W + 1][d]
     int batch, L, d, silu;
-    int run;                               // tokens of one thread's run
+    int run, across;                       // tokens of one thread's run, strips of a CTA
+    int w16;                               // w starts on a 16-byte boundary
 };
 
 namespace {
@@ -78,21 +79,42 @@ __device__ __forceinline__ void put_strip(char *at, const float (&f)[V], int lef
     }
 }
 
-// the run of tokens and the channel strip of a thread
+// the run of tokens and the channel strip of a thread: a CTA is `across` neighbouring strips by
+// kConvThreads / across runs
 struct ConvSpot {
     int b, t0, t1, c;
+    int64_t group;                         // the CTA's place among the groups of runs
+    bool any;
 };
 template <int V>
-__device__ __forceinline__ bool conv_spot(const ConvArgs &p, ConvSpot &s) {
+__device__ __forceinline__ ConvSpot conv_spot(const ConvArgs &p) {
+    ConvSpot s;
     const int strips = (p.d + V - 1) / V, runs = (p.L + p.run - 1) / p.run;
-    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t at = i / strips;
-    s.c = (int)(i % strips) * V;
-    if (at >= (int64_t)p.batch * runs) return false;
+    const int blocks = (strips + p.across - 1) / p.across;
+    s.group = blockIdx.x / blocks;
+    s.c = ((int)(blockIdx.x % blocks) * p.across + (int)threadIdx.x % p.across) * V;
+    const int64_t at = s.group * (kConvThreads / p.across) + threadIdx.x / p.across;
+    s.any = at < (int64_t)p.batch * runs && s.c < p.d;
     s.b = (int)(at / runs);
     s.t0 = (int)(at % runs) * p.run;
     s.t1 = min(s.t0 + p.run, p.L);
-    return true;
+    return s;
+}
+// taps and bias of a strip (columns past d repeat the last)
+template <int W, int V>
+__device__ __forceinline__ void conv_taps(const ConvArgs &p, int c, float (&w)[W][V], float (&bias)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int ci = min(c + i, p.d - 1);
+        bias[i] = p.b ? __ldg(p.b + ci) : 0.0f;
+        if (W == 4 && p.w16) {
+            const float4 q = __ldg(reinterpret_cast<const float4 *>(p.w) + ci);
+            w[0][i] = q.x, w[1][i] = q.y, w[W - 2][i] = q.z, w[W - 1][i] = q.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < W; ++k) w[k][i] = __ldg(p.w + (int64_t)ci * W + k);
+        }
+    }
 }
 
 // Prompts.  A thread takes `run` tokens of V channels.  Where its run starts inside a
@@ -100,18 +122,12 @@ __device__ __forceinline__ bool conv_spot(const ConvArgs &p, ConvSpot &s) {
 // the window is filled from that sequence's state row or zeros.
 template <typename T, int W, int V, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_prompt(const ConvArgs p) {
-    ConvSpot o;
-    if (!conv_spot<V>(p, o)) return;
+    const ConvSpot o = conv_spot<V>(p);
+    if (!o.any) return;
     const int left = p.d - o.c;
     const RowsOf<T> gx(p.x, o.b, o.c), gy(p.y, o.b, o.c);
     float w[W][V], bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int c = min(o.c + i, p.d - 1);
-        bias[i] = p.b ? p.b[c] : 0.0f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[k][i] = p.w[(int64_t)c * W + k];
-    }
+    conv_taps<W, V>(p, o.c, w, bias);
     int s = p.seqs.cu ? sequence_at(p.seqs, o.t0) : o.b;
     int t = o.t0;
     float win[W][V];                                       // win[k]: x at t - W + 1 + k
@@ -171,6 +187,7 @@ template <typename T, int W>
 __global__ void __launch_bounds__(kConvThreads) conv_states(const ConvArgs p) {
     const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
     const int64_t s = i / p.d;
+    cudaGridDependencySynchronize();                       // conv_prompt has read the states
     if (s >= p.seqs.n) return;
     const int c = (int)(i % p.d);
     const Seq q = sequence(p.seqs, (int)s);
@@ -208,13 +225,12 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
             x[k].load(reinterpret_cast<const char *>(static_cast<const T *>(p.state) + row + (int64_t)k * p.d), left);
     }
     x[W - 1].load(RowsOf<T>(p.x, b, c).at(0), left);
-    float y[V];
+    float w[W][V], y[V];
+    conv_taps<W, V>(p, c, w, y);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int ce = min(c + e, p.d - 1);
-        y[e] = p.b ? p.b[ce] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < W; ++k) y[e] = fmaf(p.w[(int64_t)ce * W + k], x[k].f(e), y[e]);
+        for (int k = 0; k < W; ++k) y[e] = fmaf(w[k][e], x[k].f(e), y[e]);
         if (p.silu) y[e] *= sigmoid(y[e]);
     }
     put_strip<T, V, VEC>(const_cast<char *>(RowsOf<T>(p.y, b, c).at(0)), y, left);
@@ -233,23 +249,21 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
 // dw and db take the run's own tokens.  The runs' sums go to `part`.
 template <typename T, int W, int V, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_bwd(const ConvArgs p) {
-    ConvSpot o;
-    if (!conv_spot<V>(p, o)) return;
+    const ConvSpot o = conv_spot<V>(p);
     const int left = p.d - o.c;
     const RowsOf<T> gx(p.x, o.b, o.c), go(p.dout, o.b, o.c), gdx(p.dx, o.b, o.c);
     float w[W][V], bias[V], dw[W][V], db[V];
+    conv_taps<W, V>(p, o.c, w, bias);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = min(o.c + i, p.d - 1);
-        bias[i] = p.b ? p.b[c] : 0.0f;
         db[i] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < W; ++k) w[k][i] = p.w[(int64_t)c * W + k], dw[k][i] = 0.0f;
+        for (int k = 0; k < W; ++k) dw[k][i] = 0.0f;
     }
-    int s = p.seqs.cu ? sequence_at(p.seqs, o.t0) : o.b;
+    int s = p.seqs.cu && o.any ? sequence_at(p.seqs, o.t0) : o.b;
     int t = o.t0;
 #pragma unroll 1
-    while (t < o.t1 && s < p.seqs.n) {
+    while (o.any && t < o.t1 && s < p.seqs.n) {
         const Seq q = sequence(p.seqs, s);
         const int begin = max(t, q.start), end = min(o.t1, q.end), stop = min(end + W - 1, q.end);
         if (begin < end) {
@@ -311,26 +325,34 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd(const ConvArgs p) {
         ++s;
         if (!p.seqs.cu) break;
     }
-    const int runs = (p.L + p.run - 1) / p.run;
-    float *part = p.part + ((int64_t)o.b * runs + o.t0 / p.run) * p.d * (W + 1);
+    // the runs of the CTA that share a strip, joined in shared memory in their order
+    __shared__ float sums[(W + 1) * V][kConvThreads];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        if (i >= left) break;
 #pragma unroll
-        for (int k = 0; k < W; ++k) part[(int64_t)k * p.d + o.c + i] = dw[k][i];
-        part[(int64_t)W * p.d + o.c + i] = db[i];
+        for (int k = 0; k < W; ++k) sums[k * V + i][threadIdx.x] = dw[k][i];
+        sums[W * V + i][threadIdx.x] = db[i];
+    }
+    __syncthreads();
+    const int64_t n = (int64_t)p.d * (W + 1);
+    const int c0 = o.c - (int)(threadIdx.x % p.across) * V;
+    for (int i = threadIdx.x; i < (W + 1) * V * p.across; i += kConvThreads) {
+        const int x = i % p.across, kv = i / p.across, c = c0 + x * V + kv % V;
+        float f = 0.0f;
+        for (int y = x; y < kConvThreads; y += p.across) f += sums[kv][y];
+        if (c < p.d) p.part[o.group * n + (int64_t)(kv / V) * p.d + c] = f;
     }
 }
 
-// dw [d][W] and db [d] from the runs' sums [runs][W + 1][d]
+// dw [d][W] and db [d] from the groups' sums [groups][W + 1][d]
 constexpr int kConvSumX = 32, kConvSumY = 16;
-__global__ void __launch_bounds__(kConvSumX *kConvSumY) conv_bwd_sum(const float *part, int64_t runs, int d, int W,
+__global__ void __launch_bounds__(kConvSumX *kConvSumY) conv_bwd_sum(const float *part, int64_t groups, int d, int W,
                                                                        float *dw, float *db) {
     __shared__ float sums[kConvSumY][kConvSumX];
     const int64_t n = (int64_t)d * (W + 1), i = (int64_t)blockIdx.x * kConvSumX + threadIdx.x;
     float s = 0.0f;
     if (i < n)
-        for (int64_t r = threadIdx.y; r < runs; r += kConvSumY) s += part[r * n + i];
+        for (int64_t r = threadIdx.y; r < groups; r += kConvSumY) s += part[r * n + i];
     sums[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && i < n) {
@@ -343,12 +365,24 @@ __global__ void __launch_bounds__(kConvSumX *kConvSumY) conv_bwd_sum(const float
     }
 }
 
-// tokens of a thread's run: long enough that the W - 1 tokens read twice and the partial sums
-// cost little, short enough for two rounds of threads on every SM
-int conv_run(int64_t rows, int strips, int least) {
-    const int64_t want = 148 * 2048;
-    const int64_t run = (rows * strips + want - 1) / want;
-    return (int)std::max<int64_t>(least, std::min<int64_t>(64, (run + 7) / 8 * 8));
+// How a call is cut: runs long enough that the W - 1 tokens read twice, the taps and the
+// partial sums cost little, short enough for 16 warps on every SM; strips of a CTA next to one
+// another for whole lines.
+struct ConvCut {
+    int strips, run, across, blocks;
+    int64_t groups;
+};
+ConvCut conv_cut(int batch, int L, int d, int V) {
+    ConvCut c;
+    c.strips = (d + V - 1) / V;
+    const int64_t rows = (int64_t)batch * L, want = 148 * 512;
+    c.run = (int)std::max<int64_t>(8, std::min<int64_t>(64, (rows * c.strips / want + 7) / 8 * 8));
+    c.across = 1;
+    while (c.across < 32 && c.across < c.strips) c.across *= 2;
+    c.blocks = (c.strips + c.across - 1) / c.across;
+    const int64_t runs = (int64_t)batch * ((L + c.run - 1) / c.run);
+    c.groups = (runs + kConvThreads / c.across - 1) / (kConvThreads / c.across);
+    return c;
 }
 
 // what a call's rows allow: the strip width and whether strips move as one vector
@@ -363,12 +397,11 @@ vim_status conv_launch(ConvKind kind, ConvArgs &a, bool vec8, bool vec4, cudaStr
     // prompts and tokens in 16-byte strips; the derivative, which keeps twice the registers
     // per channel, in strips of 4
     constexpr int V = Vec<T>::n;
-    const bool wide = kind != kBackward;
-    const int v = wide ? V : 4;
-    const int strips = (a.d + v - 1) / v;
-    const int64_t threads = kind == kStep ? (int64_t)a.batch * strips
-                                          : (int64_t)a.batch * ((a.L + a.run - 1) / a.run) * strips;
-    const int64_t grid = (threads + kConvThreads - 1) / kConvThreads;
+    const ConvCut cut = conv_cut(a.batch, a.L, a.d, kind == kBackward ? 4 : V);
+    a.run = cut.run, a.across = cut.across;
+    a.w16 = !misaligned(a.w, 16);
+    const int64_t grid = kind == kStep ? ((int64_t)a.batch * cut.strips + kConvThreads - 1) / kConvThreads
+                                       : cut.groups * cut.blocks;
     if (grid > INT32_MAX) return VIM_ERR_UNSUPPORTED;
     auto go = [&](auto kernel) {
         if (grid > 0) kernel<<<(unsigned)grid, kConvThreads, 0, stream>>>(a);   // none: empty sequences still have states
@@ -380,8 +413,8 @@ vim_status conv_launch(ConvKind kind, ConvArgs &a, bool vec8, bool vec4, cudaStr
     if (kind == kPrompt && a.state_out) {
         const int64_t n = ((int64_t)a.seqs.n * a.d + kConvThreads - 1) / kConvThreads;
         if (n > INT32_MAX) return VIM_ERR_UNSUPPORTED;
-        conv_states<T, W><<<(unsigned)n, kConvThreads, 0, stream>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return VIM_ERR_CUDA;
+        if (launch_dependent(conv_states<T, W>, dim3((unsigned)n), dim3(kConvThreads), 0, stream, a) != cudaSuccess)
+            return VIM_ERR_CUDA;
     }
     return VIM_OK;
 }
@@ -401,10 +434,6 @@ vim_status conv_check(int batch, int L, int d, int W, vim_dtype dt, const float 
     if (W < 2 || W > 4) return VIM_ERR_UNSUPPORTED;
     if (d > 0 && (!w || misaligned(w, 4) || misaligned(b, 4))) return VIM_ERR_INVALID_ARG;
     return VIM_OK;
-}
-
-int conv_bwd_run(int batch, int L, int d) {
-    return conv_run((int64_t)batch * L, (d + 3) / 4, 16);
 }
 
 }  // namespace
@@ -431,7 +460,6 @@ vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, in
     a.state_out = seqs ? seqs->state_out : nullptr;
     a.batch = batch, a.L = L, a.d = channels, a.silu = silu != 0;
     const int V = dt == VIM_F32 ? 4 : 8;
-    a.run = conv_run((int64_t)batch * L, (channels + V - 1) / V, 8);
     const bool vec = channels % V == 0 && conv_vec(x, batch, L, elem_size(dt), V) &&
                      conv_vec(y, batch, L, elem_size(dt), V) && !misaligned(a.state, 16);
     return dt == VIM_F32 ? conv_width<float>(kPrompt, a, width, vec, false, stream)
@@ -456,7 +484,7 @@ vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *
     if (!rows.state || bad_rows(x, dt) || bad_out(y, dt, batch, 1, channels)) return VIM_ERR_INVALID_ARG;
     a.x = x, a.y = y, a.w = w, a.b = b;
     a.state = rows.state, a.state_out = rows.state_out;
-    a.batch = batch, a.L = 1, a.d = channels, a.silu = silu != 0, a.run = 1;
+    a.batch = batch, a.L = 1, a.d = channels, a.silu = silu != 0;
     const int V = dt == VIM_F32 ? 4 : 8;
     const bool vec = channels % V == 0 && conv_vec(x, batch, 1, elem_size(dt), V) &&
                      conv_vec(y, batch, 1, elem_size(dt), V) && !misaligned(a.state, 16) && !misaligned(a.state_out, 16);
@@ -466,8 +494,7 @@ vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *
 
 size_t causal_conv_bwd_workspace_bytes(int batch, int L, int channels, int width) {
     if (batch <= 0 || L <= 0 || channels <= 0 || width < 2 || width > 4) return 0;
-    const int run = conv_bwd_run(batch, L, channels);
-    return round_up((size_t)batch * ((L + run - 1) / run) * channels * (width + 1) * sizeof(float));
+    return round_up((size_t)conv_cut(batch, L, channels, 4).groups * channels * (width + 1) * sizeof(float));
 }
 
 vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const float *b, float *dw, float *db,
@@ -500,16 +527,15 @@ vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const floa
     a.x = x, a.dout = dout, a.dx = dx, a.w = w, a.b = b;
     a.part = static_cast<float *>(workspace);
     a.batch = batch, a.L = L, a.d = channels, a.silu = silu != 0;
-    a.run = conv_bwd_run(batch, L, channels);
     const size_t el = elem_size(dt);
     const bool vec = channels % 4 == 0 && conv_vec(x, batch, L, el, 4) && conv_vec(dout, batch, L, el, 4) &&
                      conv_vec(dx, batch, L, el, 4);
     st = dt == VIM_F32 ? conv_width<float>(kBackward, a, width, false, vec, stream)
                        : conv_width<__nv_bfloat16>(kBackward, a, width, false, vec, stream);
     if (st != VIM_OK) return st;
-    const int64_t runs = (int64_t)batch * ((L + a.run - 1) / a.run), n = (int64_t)channels * (width + 1);
+    const int64_t n = (int64_t)channels * (width + 1);
     conv_bwd_sum<<<(unsigned)((n + kConvSumX - 1) / kConvSumX), dim3(kConvSumX, kConvSumY), 0, stream>>>(
-        a.part, runs, channels, width, dw, db);
+        a.part, conv_cut(batch, L, channels, 4).groups, channels, width, dw, db);
     return cudaGetLastError() == cudaSuccess ? VIM_OK : VIM_ERR_CUDA;
 }
 
