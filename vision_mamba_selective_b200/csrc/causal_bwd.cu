@@ -54,7 +54,7 @@ __device__ __forceinline__ float reduce_channels(float (&v)[n], int cl) {
 // instructions with the sums over lanes (dB and dC over channels, three sums over states)
 // and the per-token functions.
 template <typename T, int N, int NL, bool PACKED>
-__global__ void __launch_bounds__(32 * kBwdWarps, 3) causal_bwd_main(const CausalBwdArgs p) {
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const CausalBwdArgs p) {
     constexpr int LPC = N / NL, CH = 32 / LPC, NP = NL / 2, EPL = kSeg / LPC, NV = 2 * NL;
     constexpr int SEGS = kAdjEvery / kSeg;
     __shared__ __align__(16) float Bs[kAdjEvery * N], Cs[kAdjEvery * N];
@@ -339,9 +339,9 @@ CausalBwdPlan causal_bwd_plan(int batch, int L, int d, int N, bool has_ckpt) {
     pl.chunks = (int64_t)batch * pl.chunks_per_row;
     const int ch = N == 16 ? 8 : N == 2 ? 32 : 16;
     const int blocks = (d + ch * kBwdWarps - 1) / (ch * kBwdWarps);
-    // enough CTAs for two rounds on every SM, three at a time there; more slices only cost
+    // enough CTAs for two rounds on every SM, two at a time there; more slices only cost
     // traffic (each leaves 2 N sums per token)
-    const int64_t want = 148 * 3 * 2;
+    const int64_t want = 148 * 2 * 2;
     const int64_t s = std::max<int64_t>(1, std::min<int64_t>(blocks, (want + pl.chunks - 1) / std::max<int64_t>(pl.chunks, 1)));
     pl.blocks_per_slice = (int)((blocks + s - 1) / s);
     pl.slices = (blocks + pl.blocks_per_slice - 1) / pl.blocks_per_slice;
