@@ -27,9 +27,8 @@ inline bool bad_out(const vim_rows &r, vim_dtype dt, int batch, int L, int width
     if (L > 1 && r.row_stride < width) return true;
     return batch > 1 && r.batch_stride < (int64_t)(L - 1) * r.row_stride + width;
 }
-// whether every row of r (B or C) can be read in vectors of N / 4 elements
-inline bool lane_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int N) {
-    const int n = N >= 4 ? N / 4 : 1;
+// whether every row of r can be read in vectors of n elements
+inline bool row_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int n) {
     return !misaligned(r.data, n * elem_size(dt)) && (L <= 1 || r.row_stride % n == 0) &&
            (batch <= 1 || r.batch_stride % n == 0);
 }

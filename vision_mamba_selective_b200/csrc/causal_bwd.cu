@@ -56,7 +56,6 @@ __device__ __forceinline__ float reduce_channels(float (&v)[n], int cl) {
 template <typename T, int N, int NL, bool PACKED>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const CausalBwdArgs p) {
     constexpr int LPC = N / NL, CH = 32 / LPC, NP = NL / 2, EPL = kSeg / LPC, NV = 2 * NL;
-    constexpr int SEGS = kAdjEvery / kSeg;
     __shared__ __align__(16) float Bs[kAdjEvery * N], Cs[kAdjEvery * N];
     __shared__ float acc[kBwdWarps][2][kAdjEvery * N];     // dB, dC
     __shared__ unsigned flags[3][2];                       // tokens of a sequence, its first, its last
@@ -107,6 +106,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const Causa
     const int cb0 = slice * p.blocks_per_slice, cb1 = min(cb0 + p.blocks_per_slice, cblocks);
     const int64_t kept_row = (int64_t)b * ((L + kCkEvery - 1) / kCkEvery) + t0 / kCkEvery;
     const int64_t chunk = blockIdx.x;
+    const int last_kept = (min(L - t0, kAdjEvery) - 1) / kSeg;
 
 #pragma unroll 1
     for (int cb = cb0; cb < cb1; ++cb) {
@@ -128,21 +128,18 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const Causa
         const bool goes_on = PACKED ? (in_hi >> 31) && !(last_hi >> 31) : t0 + kAdjEvery < L;
         if (goes_on) load_row<NP>(p.adj + (chunk * p.d + c) * N + q * NL, g);
 
-        const int top = PACKED ? SEGS - 1 : (min(L - t0, kAdjEvery) - 1) / kSeg;
+        const int top = last_kept;
         uint32_t ru[EPL], rd[EPL], rz[EPL], ro[EPL];
         float2 hk[NP];
         auto fetch = [&](int seg) {
-            const unsigned in = bits(in_lo, in_hi, seg);
 #pragma unroll
             for (int e = 0; e < EPL; ++e) {
-                const int r = e * LPC + q, t = t0 + seg * kSeg + r;
-                ru[e] = rd[e] = rz[e] = ro[e] = 0;
-                if (in >> r & 1u) {
-                    ru[e] = gu.raw(t), rd[e] = gd.raw(t), rz[e] = gz.raw(t), ro[e] = go.raw(t);
-                }
+                // past the row's end its last token is read, and dropped
+                const int t = min(t0 + seg * kSeg + e * LPC + q, L - 1);
+                ru[e] = gu.raw(t), rd[e] = gd.raw(t), rz[e] = gz.raw(t), ro[e] = go.raw(t);
             }
-            // (a segment that no sequence enters holds nothing here; its first token resets)
-            if (in) load_row<NP>(p.ckpt + ((kept_row + seg) * p.d + c) * N + q * NL, hk);
+            // (where no sequence enters a segment nothing was kept; its first token resets)
+            load_row<NP>(p.ckpt + ((kept_row + min(seg, last_kept)) * p.d + c) * N + q * NL, hk);
         };
         fetch(top);
 #pragma unroll 1
@@ -157,16 +154,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const Causa
                 // lanes past d run the last channel with nothing flowing in: their sums are zero
                 const bool ok = live && (in >> (e * LPC + q) & 1u);
                 u[e] = bits_f32<T>(ru[e]);
-                const float z = bits_f32<T>(rz[e]), o = ok ? bits_f32<T>(ro[e]) : 0.0f;
+                const float z = bits_f32<T>(rz[e]), o = bits_f32<T>(ro[e]);
                 dt[e] = ok ? softplus_slope(bits_f32<T>(rd[e]) + bias, slope[e]) : 0.0f;
                 const float sg = sigmoid(z);
                 x[e] = ok ? dt[e] * u[e] : 0.0f;
-                dy[e] = gate ? o * (z * sg) : o;
+                dy[e] = ok ? (gate ? o * (z * sg) : o) : 0.0f;
                 dgate[e] = o * (sg * fmaf(z, 1.0f - sg, 1.0f));
             }
             float2 h[NP];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) h[i] = in ? hk[i] : f2(0.0f, 0.0f);
+            for (int i = 0; i < NP; ++i) h[i] = hk[i];
             if (seg > 0) fetch(seg - 1);
 
             // where the lane adds its sum over channels of token pair (r, r + 1)
@@ -420,7 +417,7 @@ vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const floa
     pass.u = u, pass.delta = delta, pass.z = z, pass.B = B, pass.C = C, pass.dout = dout;
     pass.A = A, pass.D = D, pass.bias = delta_bias;
     pass.d = d_inner;
-    pass.vec_bc = lane_vectors(B, dt, batch, L, d_state) && lane_vectors(C, dt, batch, L, d_state);
+    pass.vec_bc = row_vectors(B, dt, batch, L, lane_states(d_state)) && row_vectors(C, dt, batch, L, lane_states(d_state));
     if (!ckpt) {
         pass.ckpt = at(pl.o_ckpt);
         st = launch_pass<kStates>(pass, d_state, dt, stream);

@@ -285,6 +285,9 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
 
 }  // namespace
 
+// states of B (C) that a lane fetches of a segment
+inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
+
 // Warps per CTA.  Eight keep two CTAs an SM busy; four waste less of a short row when
 // there are channels enough to fill the GPU anyway (64 rows of 197 tokens, 768 channels,
 // N = 16, bf16: 102 us with four, 117 with eight; 8 rows of 4097 tokens, 384 channels: 152
