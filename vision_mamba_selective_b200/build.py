@@ -24,7 +24,7 @@ def sources():
 
 def deps():
     return sources() + sorted(glob.glob(os.path.join(PKG, "csrc", "*.cuh"))) + [
-        os.path.join(ROOT, "include", "vimscan.h")]
+        os.path.join(ROOT, "include", h) for h in ("vimscan.h", "vimscan_causal.h")]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -1,4 +1,4 @@
-// causal.cu -- entry points of the causal selective scan (declared in include/vimscan.h)
+// causal.cu -- entry points of the causal selective scan (declared in include/vimscan_causal.h)
 // and its single-token kernel.
 #include "causal_kernels.cuh"
 

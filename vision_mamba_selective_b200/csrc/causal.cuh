@@ -2,7 +2,7 @@
 // (scan, short convolution, their single-token forms and derivatives).
 #pragma once
 
-#include "vimscan.h"
+#include "vimscan_causal.h"
 
 #include <cstdint>
 

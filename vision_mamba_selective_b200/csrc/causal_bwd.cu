@@ -1,4 +1,4 @@
-// causal_bwd.cu -- derivative of the causal selective scan (declared in include/vimscan.h).
+// causal_bwd.cu -- derivative of the causal selective scan (declared in include/vimscan_causal.h).
 //
 // With dy = dout silu(z), g_t = C_t dy_t + exp(Delta_(t+1) A) g_(t+1) and
 // m_t = exp(Delta_t A) h_(t-1), per token and channel

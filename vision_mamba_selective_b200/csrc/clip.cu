@@ -1,5 +1,5 @@
 // clip.cu -- the common norm of many gradient tensors, and clipping by it (declared in
-// include/vimscan.h).
+// include/vimscan_causal.h).
 //
 //   norm = sqrt(sum_i |g_i|^2),   out_i = g_i min(1, max_norm / (norm + 1e-6))
 //
@@ -176,7 +176,8 @@ bool clip_overlap(const vim_tensor *t, int count) {
     return false;
 }
 
-int clip_launches(int count) { return count < 1 ? 1 : (count + kPerLaunch - 1) / kPerLaunch; }
+int clip_launches(int count) { return count < 1 ? 1 : (count - 1) / kPerLaunch + 1; }
+size_t clip_bytes(int count) { return round_up((size_t)clip_launches(count) * kClipCtas * sizeof(double)); }
 
 vim_status clip_impl(const vim_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
                      size_t workspace_bytes, cudaStream_t stream) {
@@ -193,7 +194,7 @@ vim_status clip_impl(const vim_tensor *tensors, int count, float max_norm, float
     }
     if (clip_overlap(tensors, count)) return VIM_ERR_INVALID_ARG;
     const int launches = clip_launches(count), parts = launches * kClipCtas;
-    if (!workspace || workspace_bytes < parts * sizeof(double) || misaligned(workspace, kAlign)) return VIM_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < clip_bytes(count) || misaligned(workspace, kAlign)) return VIM_ERR_WORKSPACE;
     double *part = static_cast<double *>(workspace);
     auto table = [&](int launch, ClipTable &t) {
         std::memset(&t, 0, sizeof(t));
@@ -233,7 +234,7 @@ using namespace vimscan;
 extern "C" {
 
 size_t clip_grad_norm_workspace_bytes(int count) {
-    return count < 0 ? 0 : round_up((size_t)clip_launches(count) * kClipCtas * sizeof(double));
+    return count < 0 ? 0 : clip_bytes(count);
 }
 
 vim_status clip_grad_norm(const vim_tensor *tensors, int count, float max_norm, float *norm, void *workspace,

@@ -1,4 +1,4 @@
-// conv.cu -- short causal depthwise convolution (declared in include/vimscan.h): prompts,
+// conv.cu -- short causal depthwise convolution (declared in include/vimscan_causal.h): prompts,
 // single tokens and the derivative.
 //
 //   pre_t = b + sum_(k < W) w_k x_(t - W + 1 + k),   y_t = silu(pre_t) or pre_t

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libvimscan.so (declared in include/vimscan.h).
+"""Thin ctypes binding of libvimscan.so (declared in include/vimscan.h and, for the causal
+operators, include/vimscan_causal.h).
 
 Argument marshalling only: every tensor is checked for device (the current CUDA
 device), dtype, shape and contiguity before the library is called, then turned into
@@ -865,7 +866,7 @@ def causal_ckpt_shape(batch, L, d_inner, d_state):
 
 def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=None, state_out=None, slots=None,
                 fresh=None, ckpt=None, y=None, stream=None):
-    """Causal selective scan; see include/vimscan.h.
+    """Causal selective scan; see include/vimscan_causal.h.
 
     u, delta, z: [batch, L, d_inner], or [tokens, d_inner] with ``cu_seqlens`` (int32,
     n_seqs + 1 offsets of packed sequences); z may be None.  B, C: the same rows with
@@ -945,7 +946,7 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
                     stream=None):
     """Derivatives of causal_scan, for sequences that start from zeros and whose final states
     are not used, and a loss whose derivative with respect to y is ``dout``; see
-    include/vimscan.h.
+    include/vimscan_causal.h.
 
     Returns a dict: du, ddelta (w.r.t. the raw delta), dz (None without z), shaped like u in
     its dtype; dB and dC (fp32, contiguous, shaped like B); dA [d_inner, d_state], dD and
@@ -997,7 +998,7 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
 def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=None, slots=None, fresh=None, y=None,
                 stream=None):
     """Short causal depthwise convolution, with SiLU unless ``silu`` is false; see
-    include/vimscan.h.
+    include/vimscan_causal.h.
 
     x: [batch, L, channels], or [tokens, channels] with ``cu_seqlens``, any row strides.  w:
     [channels, width] fp32, width 2 to 4, the newest tap last; b: [channels] fp32 or None.
@@ -1057,7 +1058,7 @@ def causal_conv_bwd_workspace_bytes(batch, L, channels, width):
 def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None, out=None, stream=None):
     """Derivatives of causal_conv, for sequences that start from zeros and whose final states
     are not used, and a loss whose derivative with respect to y is ``dout``; see
-    include/vimscan.h.
+    include/vimscan_causal.h.
 
     Returns a dict: dx, shaped like x in its dtype; dw [channels, width] and db [channels]
     (None without b) in fp32.  ``out`` may hold those tensors from an earlier call (dx with
@@ -1113,7 +1114,7 @@ def _refuse_gradient(where, name, t, dev):
 
 
 def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
-    """The common norm of many gradients, and clipping by it; see include/vimscan.h.
+    """The common norm of many gradients, and clipping by it; see include/vimscan_causal.h.
 
     ``grads``: contiguous CUDA tensors, fp32 or bf16 in any mixture, as a list or tuple, or a
     dict of them as the *_bwd functions return (None entries are skipped).  They are scaled
