@@ -225,8 +225,10 @@ struct RowsOf {
 };
 
 template <int NP> __device__ __forceinline__ void store_row(float *row, const float2 (&v)[NP]) {
-    if constexpr (NP == 2) {
-        *reinterpret_cast<float4 *>(row) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    if constexpr (NP >= 2) {
+#pragma unroll
+        for (int i = 0; i < NP; i += 2)
+            *reinterpret_cast<float4 *>(row + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
     } else {
         *reinterpret_cast<float2 *>(row) = v[0];
     }

@@ -16,7 +16,7 @@
 // on its scheduler a warp issues an instruction every four clocks.
 //
 // The walk is shared by the W warps of a CTA, which all hold the same few channels and
-// take segments of 8 tokens in turn.  For its segment a warp
+// take segments of SEG tokens (8, or 4) in turn.  For its segment a warp
 //   1. forms Delta and Delta u of its tokens, each lane its share (exchanged by shuffles);
 //   2. runs the segment from h = 0, multiplying up its decays: with P_t the product so far,
 //      h_t = P_t h_in + hz_t, and C_t . h_t = C_t . hz_t + (C_t P_t) . h_in; C_t P_t and the
@@ -64,7 +64,7 @@ enum CausalMode {
 
 namespace {
 
-constexpr int kSeg = 8;             // tokens per segment
+constexpr int kSeg = 8;             // most tokens of a segment
 constexpr int kPassWarps = 8;       // most warps of a CTA: one named barrier each
 static_assert(kCkEvery == kSeg && kAdjEvery % kSeg == 0, "kept states lie at segment borders");
 
@@ -86,26 +86,27 @@ __device__ __forceinline__ float reduce_scatter(float (&p)[n], int q) {
 }
 
 // one warp's shared memory
-template <int N, int NL>
+template <int N, int NL, int SEG>
 struct PassWarp {
     static constexpr int kLanes = N / NL;                  // lanes per channel
     static constexpr int kCh = 32 / kLanes;                // channels per warp
-    alignas(16) float bc[2][kSeg * N];                     // B and C of its segment
+    alignas(16) float bc[2][SEG * N];                     // B and C of its segment
     alignas(16) float carry[32 * NL];                      // the state handed to it, by lane
 };
 
 __device__ __forceinline__ void named_wait(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void named_arrive(int id) { asm volatile("barrier.arrive %0, 64;" ::"r"(id) : "memory"); }
 
-template <typename T, int N, int NL, int MODE, bool KEEP, bool VEC>
+template <typename T, int N, int NL, int SEG, int MODE, bool KEEP, bool VEC>
 __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalArgs p) {
-    using S = PassWarp<N, NL>;
+    using S = PassWarp<N, NL, SEG>;
     constexpr int LPC = S::kLanes, CH = S::kCh, NP = NL / 2;
-    constexpr int EPL = kSeg / LPC;                        // tokens of a segment per lane
-    constexpr int PV = kSeg * N >= 32 ? kSeg * N / 32 : 1; // B (C) values a lane fetches per segment
+    constexpr int EPL = SEG / LPC;                        // tokens of a segment per lane
+    constexpr int PV = SEG * N >= 32 ? SEG * N / 32 : 1; // B (C) values a lane fetches per segment
     constexpr bool HAS_Z = MODE != kStates, HAS_B = MODE != kAdjoint, HAS_C = MODE != kStates;
     extern __shared__ __align__(16) unsigned char pass_smem[];
-    const int W = blockDim.x / 32, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (the warp's number by a shuffle, so that it and all that follows from it is seen to be uniform)
+    const int W = blockDim.x / 32, w = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     S &sm = reinterpret_cast<S *>(pass_smem)[w];
     S &next = reinterpret_cast<S *>(pass_smem)[w + 1 == W ? 0 : w + 1];
 
@@ -124,21 +125,17 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
     const int at = lane * PV;                              // the lane's B (C) values: token, state
     const RowsOf<T> gB(p.B, b, at % N), gC(p.C, b, at % N);
 
-    float2 A2[NP], h0[NP];
+    float2 A2[NP];
     load_row<NP>(p.A + (int64_t)c * N + q * NL, A2);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        A2[i] = mul2(A2[i], f2(kLog2e, kLog2e));
-        h0[i] = f2(0.0f, 0.0f);
-    }
-    if (p.state && !seq.fresh) load_row<NP>(p.state + (seq.slot * p.d + c) * N + q * NL, h0);
+    for (int i = 0; i < NP; ++i) A2[i] = mul2(A2[i], f2(kLog2e, kLog2e));
     const float bias = p.bias[c], Dc = MODE == kForward ? p.D[c] : 0.0f;
 
     // segments of the sequence; m = 0 is the first in the order of the walk
-    const int first = seq.start / kSeg;
-    const int M = seq.end > seq.start ? (seq.end + kSeg - 1) / kSeg - first : 0;
+    const int first = seq.start / SEG;
+    const int M = seq.end > seq.start ? (seq.end + SEG - 1) / SEG - first : 0;
     const unsigned length = seq.end - seq.start;
-    auto seg_at = [&](int m) { return (MODE == kAdjoint ? first + M - 1 - m : first + m) * kSeg; };
+    auto seg_at = [&](int m) { return (MODE == kAdjoint ? first + M - 1 - m : first + m) * SEG; };
 
     // as loaded: anything done to the bits here would wait for the load
     constexpr int PW = PV == 1 ? 1 : PV * (int)sizeof(T) / 4;
@@ -165,6 +162,15 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
         }
     };
 
+    if (w == 0) {                                          // the sequence's initial state is the first carry
+        float2 h0[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) h0[i] = f2(0.0f, 0.0f);
+        if (p.state && !seq.fresh) load_row<NP>(p.state + (seq.slot * p.d + c) * N + q * NL, h0);
+        store_row<NP>(&sm.carry[lane * NL], h0);
+        if (M == 0 && MODE != kStates && p.state_out && live)
+            store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, h0);
+    }
     if (w < M) fetch(w);
 #pragma unroll 1
     for (int m = w; m < M; m += W) {
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
             }
             if constexpr (PV == 4) {
                 *reinterpret_cast<float4 *>(&sm.bc[k][at]) = make_float4(f[0], f[1], f[2], f[3]);
-            } else if (at < kSeg * N) {
+            } else if (at < SEG * N) {
 #pragma unroll
                 for (int i = 0; i < PV; ++i) sm.bc[k][at + i] = f[i];
             }
@@ -206,10 +212,10 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
         __syncwarp();
 
         // 2. the segment from zero, the product of its decays so far, and what y takes of both
-        float2 reach[MODE == kForward ? kSeg : 1][NP], part0[MODE == kForward ? kSeg : 1], P[NP], hz[NP];
+        float2 reach[MODE == kForward ? SEG : 1][NP], part0[MODE == kForward ? SEG : 1], P[NP], hz[NP];
 #pragma unroll
-        for (int jj = 0; jj < kSeg; ++jj) {
-            const int j = MODE == kAdjoint ? kSeg - 1 - jj : jj;
+        for (int jj = 0; jj < SEG; ++jj) {
+            const int j = MODE == kAdjoint ? SEG - 1 - jj : jj;
             const float dt = __shfl_sync(0xffffffffu, dt_own[j / LPC], j % LPC * CH + cl);
             const float x1 = __shfl_sync(0xffffffffu, x_own[j / LPC], j % LPC * CH + cl);
             float2 rowB[NP], rowC[NP];
@@ -235,13 +241,8 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
 
         // 3. the state entering the segment, and the one leaving it
         float2 h[NP], out[NP];
-        if (m == 0) {
-#pragma unroll
-            for (int i = 0; i < NP; ++i) h[i] = h0[i];
-        } else {
-            if (W > 1) named_wait(w);
-            load_row<NP>(&sm.carry[lane * NL], h);
-        }
+        if (m > 0 && W > 1) named_wait(w);
+        load_row<NP>(&sm.carry[lane * NL], h);
 #pragma unroll
         for (int i = 0; i < NP; ++i) out[i] = fma2(P[i], h[i], hz[i]);
         if (m + 1 < M) {
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
         } else if (MODE != kStates && p.state_out && live) {
             store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, out);
         }
-        if (KEEP && MODE != kAdjoint && t0 >= seq.start && live) {
+        if (KEEP && MODE != kAdjoint && (SEG == kCkEvery || t0 % kCkEvery == 0) && t0 >= seq.start && live) {
             const int64_t row = b * ((p.seqs.L + kCkEvery - 1) / kCkEvery) + t0 / kCkEvery;
             store_row<NP>(p.ckpt + (row * p.d + c) * N + q * NL, h);
         }
@@ -279,8 +280,6 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
         }
         __syncwarp();                                      // the warp's shared memory may be written again
     }
-    if (M == 0 && w == 0 && MODE != kStates && p.state_out && live)
-        store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, h0);
 }
 
 }  // namespace
@@ -288,14 +287,28 @@ __global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalAr
 // states of B (C) that a lane fetches of a segment
 inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 
-// Warps per CTA.  Eight keep two CTAs an SM busy; four waste less of a short row when
-// there are channels enough to fill the GPU anyway (64 rows of 197 tokens, 768 channels,
-// N = 16, bf16: 102 us with four, 117 with eight; 8 rows of 4097 tokens, 384 channels: 152
-// and 143).  A row has no work for more warps than it has segments.
-inline int pass_warps(int64_t channels, int L) {
-    const int most = channels >= 16384 && L < 1024 ? 4 : kPassWarps;
-    const int segments = (L + kSeg - 1) / kSeg;
-    return segments >= most ? most : segments < 1 ? 1 : segments;
+// How a call is cut: states a lane holds, tokens of a segment, warps of a CTA.
+//   - Eight states and segments of 4 (16 channels a warp, 32-byte rows at bf16) need fewer
+//     loads, shuffles and selects per token-channel than four and segments of 8, but half
+//     the CTAs and twice the handovers per token: better from 8192 channels on (11 packed
+//     sequences x 2048 channels: 147 us against 164; 4 x 2048 tokens x 4096: 279 and 301),
+//     worse below (1 x 4096 tokens x 2048 channels: 113 and 92).
+//   - Eight warps hide the handover best; four waste less where sequences are short
+//     (64 x 16 tokens x 4096 channels: 68 us against 115; 16 x 200 x 2048: 61 and 68; 64 x
+//     500 x 768: 203 and 209; the 11 packed sequences above, 745 tokens on average: 162 and
+//     147).  A row has no work for more warps than segments.
+struct PassPlan {
+    int states, seg, warps;
+};
+inline PassPlan pass_plan(int N, int64_t channels, int64_t tokens_per_seq, int L) {
+    PassPlan pl;
+    const bool thick = N == 16 && channels >= 8192;
+    pl.states = thick ? 8 : N >= 8 ? 4 : 2;
+    pl.seg = thick ? 4 : kSeg;
+    pl.warps = tokens_per_seq < 256 ? 4 : kPassWarps;
+    const int segments = (L + pl.seg - 1) / pl.seg;
+    if (segments < pl.warps) pl.warps = segments < 1 ? 1 : segments;
+    return pl;
 }
 
 template <int MODE>

@@ -7,14 +7,14 @@
 namespace vimscan {
 namespace {
 
-template <typename T, int N, int NL, int MODE>
+template <typename T, int N, int NL, int SEG, int MODE>
 vim_status launch_pass_v(const CausalArgs &a, int warps, cudaStream_t stream) {
-    using S = PassWarp<N, NL>;
+    using S = PassWarp<N, NL, SEG>;
     const int64_t grid = (int64_t)a.seqs.n * ((a.d + S::kCh - 1) / S::kCh);
     if (grid > INT32_MAX) return VIM_ERR_UNSUPPORTED;
     constexpr bool ALWAYS = MODE != kForward;              // the other modes are there to keep states
-    auto kernel = ALWAYS || a.ckpt ? (a.vec_bc ? causal_pass<T, N, NL, MODE, true, true> : causal_pass<T, N, NL, MODE, true, false>)
-                                   : (a.vec_bc ? causal_pass<T, N, NL, MODE, ALWAYS, true> : causal_pass<T, N, NL, MODE, ALWAYS, false>);
+    auto kernel = ALWAYS || a.ckpt ? (a.vec_bc ? causal_pass<T, N, NL, SEG, MODE, true, true> : causal_pass<T, N, NL, SEG, MODE, true, false>)
+                                   : (a.vec_bc ? causal_pass<T, N, NL, SEG, MODE, ALWAYS, true> : causal_pass<T, N, NL, SEG, MODE, ALWAYS, false>);
     static_assert(kPassWarps * sizeof(S) <= 48 * 1024, "no opt-in for shared memory");
     kernel<<<(unsigned)grid, 32 * warps, warps * sizeof(S), stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? VIM_OK : VIM_ERR_CUDA;
@@ -22,12 +22,15 @@ vim_status launch_pass_v(const CausalArgs &a, int warps, cudaStream_t stream) {
 
 template <typename T, int MODE>
 vim_status launch_pass_t(const CausalArgs &a, int N, cudaStream_t stream) {
-    const int warps = pass_warps((int64_t)a.seqs.n * a.d, a.seqs.L);
+    const Seqs &q = a.seqs;
+    const PassPlan pl = pass_plan(N, (int64_t)q.n * a.d, q.cu ? q.L / q.n : q.L, q.L);
     switch (N) {
-        case 2: return launch_pass_v<T, 2, 2, MODE>(a, warps, stream);
-        case 4: return launch_pass_v<T, 4, 2, MODE>(a, warps, stream);
-        case 8: return launch_pass_v<T, 8, 4, MODE>(a, warps, stream);
-        default: return launch_pass_v<T, 16, 4, MODE>(a, warps, stream);
+        case 2: return launch_pass_v<T, 2, 2, 8, MODE>(a, pl.warps, stream);
+        case 4: return launch_pass_v<T, 4, 2, 8, MODE>(a, pl.warps, stream);
+        case 8: return launch_pass_v<T, 8, 4, 8, MODE>(a, pl.warps, stream);
+        default:
+            return pl.states == 8 ? launch_pass_v<T, 16, 8, 4, MODE>(a, pl.warps, stream)
+                                  : launch_pass_v<T, 16, 4, 8, MODE>(a, pl.warps, stream);
     }
 }
 
