@@ -97,8 +97,11 @@ struct PassWarp {
 __device__ __forceinline__ void named_wait(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void named_arrive(int id) { asm volatile("barrier.arrive %0, 64;" ::"r"(id) : "memory"); }
 
+// CTAs of kPassWarps on an SM: the modes without outputs hold fewer registers
+constexpr int pass_ctas(int mode) { return mode == kForward ? 2 : 3; }
+
 template <typename T, int N, int NL, int SEG, int MODE, bool KEEP, bool VEC>
-__global__ void __launch_bounds__(32 * kPassWarps, 2) causal_pass(const CausalArgs p) {
+__global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(const CausalArgs p) {
     using S = PassWarp<N, NL, SEG>;
     constexpr int LPC = S::kLanes, CH = S::kCh, NP = NL / 2;
     constexpr int EPL = SEG / LPC;                        // tokens of a segment per lane
@@ -296,16 +299,19 @@ inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 //   - Eight warps hide the handover best; four waste less where sequences are short
 //     (64 x 16 tokens x 4096 channels: 68 us against 115; 16 x 200 x 2048: 61 and 68; 64 x
 //     500 x 768: 203 and 209; the 11 packed sequences above, 745 tokens on average: 162 and
-//     147).  A row has no work for more warps than segments.
+//     147), and where the CTAs then run in one round instead of a full and a partial one
+//     (8 x 4097 tokens x 384 channels: 141 and 151).  A row has no work for more warps than
+//     segments.
 struct PassPlan {
     int states, seg, warps;
 };
-inline PassPlan pass_plan(int N, int64_t channels, int64_t tokens_per_seq, int L) {
+inline PassPlan pass_plan(int mode, int N, int64_t channels, int64_t tokens_per_seq, int L) {
     PassPlan pl;
     const bool thick = N == 16 && channels >= 8192;
     pl.states = thick ? 8 : N >= 8 ? 4 : 2;
     pl.seg = thick ? 4 : kSeg;
-    pl.warps = tokens_per_seq < 256 ? 4 : kPassWarps;
+    const int64_t ctas = channels * N / pl.states / 32, slots = 148 * pass_ctas(mode);
+    pl.warps = tokens_per_seq < 256 || (ctas > slots && ctas <= 2 * slots) ? 4 : kPassWarps;
     const int segments = (L + pl.seg - 1) / pl.seg;
     if (segments < pl.warps) pl.warps = segments < 1 ? 1 : segments;
     return pl;
