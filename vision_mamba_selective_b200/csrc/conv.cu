@@ -22,6 +22,7 @@ struct ConvArgs {
     float *part;                           // derivative: [groups of runs][W + 1][d]
     int batch, L, d, silu;
     int run, across;                       // tokens of one thread's run, strips of a CTA
+    int ctas;                              // CTAs of conv_prompt that walk tokens
     int w16;                               // w starts on a 16-byte boundary
 };
 
@@ -63,6 +64,7 @@ struct Strip {
         if constexpr (!VEC) return bits_f32<T>(v[i]);
         else return word_f32<T>(v[i * (int)sizeof(T) / 4], i);
     }
+    __device__ __forceinline__ float2 pair(int i) const { return f2(f(2 * i), f(2 * i + 1)); }
 };
 template <typename T, int V, bool VEC>
 __device__ __forceinline__ void put_strip(char *at, const float (&f)[V], int left) {
@@ -100,37 +102,73 @@ __device__ __forceinline__ ConvSpot conv_spot(const ConvArgs &p) {
     s.t1 = min(s.t0 + p.run, p.L);
     return s;
 }
-// taps and bias of a strip (columns past d repeat the last)
+// taps and bias of a strip, as pairs of channels for the packed arithmetic (columns past d
+// repeat the last)
 template <int W, int V>
-__device__ __forceinline__ void conv_taps(const ConvArgs &p, int c, float (&w)[W][V], float (&bias)[V]) {
+__device__ __forceinline__ void conv_taps(const ConvArgs &p, int c, float2 (&w)[W][V / 2], float2 (&bias)[V / 2]) {
+    auto at = [](float2 &v, int i) -> float & { return i % 2 ? v.y : v.x; };
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int ci = min(c + i, p.d - 1);
-        bias[i] = p.b ? __ldg(p.b + ci) : 0.0f;
+        at(bias[i / 2], i) = p.b ? __ldg(p.b + ci) : 0.0f;
         if (W == 4 && p.w16) {
             const float4 q = __ldg(reinterpret_cast<const float4 *>(p.w) + ci);
-            w[0][i] = q.x, w[1][i] = q.y, w[W - 2][i] = q.z, w[W - 1][i] = q.w;
+            at(w[0][i / 2], i) = q.x, at(w[1][i / 2], i) = q.y;
+            at(w[W - 2][i / 2], i) = q.z, at(w[W - 1][i / 2], i) = q.w;
         } else {
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = __ldg(p.w + (int64_t)ci * W + k);
+            for (int k = 0; k < W; ++k) at(w[k][i / 2], i) = __ldg(p.w + (int64_t)ci * W + k);
         }
     }
+}
+__device__ __forceinline__ float2 sigmoid2(float2 x) { return f2(sigmoid(x.x), sigmoid(x.y)); }
+
+// The last W - 1 inputs of sequence s and channel c, into its state row: all are read before any
+// is written, so the row may be the one that was read.
+template <typename T, int W>
+__device__ __forceinline__ void conv_last(const ConvArgs &p, int64_t s, int c) {
+    const Seq q = sequence(p.seqs, (int)s);
+    if (q.slot < 0) return;
+    const RowsOf<T> gx(p.x, p.seqs.cu ? 0 : s, c);
+    const int64_t row = q.slot * (W - 1) * p.d + c;
+    T v[W - 1];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        const int at = q.end - (W - 1) + k;
+        v[k] = from_f32<T>(0.0f);
+        if (at >= q.start) v[k] = *reinterpret_cast<const T *>(gx.at(at));
+        else if (p.state && !q.fresh) v[k] = static_cast<const T *>(p.state)[row + (int64_t)(at - q.start + W - 1) * p.d];
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) static_cast<T *>(p.state_out)[row + (int64_t)k * p.d] = v[k];
+}
+// the same as a launch of its own, for states that conv_prompt reads where they are to be written
+template <typename T, int W>
+__global__ void __launch_bounds__(kConvThreads) conv_states(const ConvArgs p) {
+    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+    cudaGridDependencySynchronize();
+    if (i < (int64_t)p.seqs.n * p.d) conv_last<T, W>(p, i / p.d, (int)(i % p.d));
 }
 
 // Prompts.  A thread takes `run` tokens of V channels.  Where its run starts inside a
 // sequence it first reads the W - 1 tokens before it, and where a sequence starts in the run
 // the window is filled from that sequence's state row or zeros.
 template <typename T, int W, int V, bool VEC>
-__global__ void __launch_bounds__(kConvThreads) conv_prompt(const ConvArgs p) {
+__global__ void __launch_bounds__(kConvThreads, 4) conv_prompt(const ConvArgs p) {
+    if ((int)blockIdx.x >= p.ctas) {                       // final states, to another buffer than the initial ones
+        const int64_t i = (int64_t)(blockIdx.x - p.ctas) * kConvThreads + threadIdx.x;
+        if (i < (int64_t)p.seqs.n * p.d) conv_last<T, W>(p, i / p.d, (int)(i % p.d));
+        return;
+    }
     const ConvSpot o = conv_spot<V>(p);
     if (!o.any) return;
     const int left = p.d - o.c;
     const RowsOf<T> gx(p.x, o.b, o.c), gy(p.y, o.b, o.c);
-    float w[W][V], bias[V];
+    float2 w[W][V / 2], bias[V / 2];
     conv_taps<W, V>(p, o.c, w, bias);
     int s = p.seqs.cu ? sequence_at(p.seqs, o.t0) : o.b;
     int t = o.t0;
-    float win[W][V];                                       // win[k]: x at t - W + 1 + k
+    float2 win[W][V / 2];                                  // win[k]: x at t - W + 1 + k
 #pragma unroll 1
     while (t < o.t1 && s < p.seqs.n) {
         const Seq q = sequence(p.seqs, s);
@@ -151,24 +189,32 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt(const ConvArgs p) {
                 x.load(reinterpret_cast<const char *>(static_cast<const T *>(p.state) +
                                                       (q.slot * (W - 1) + (at - q.start + W - 1)) * p.d + o.c), left);
 #pragma unroll
-            for (int i = 0; i < V; ++i) win[k][i] = x.f(i);
+            for (int i = 0; i < V / 2; ++i) win[k][i] = x.pair(i);
         }
-        constexpr int AHEAD = 8;                           // tokens loaded together
+        constexpr int AHEAD = 8;                           // tokens loaded together, a turn ahead
+        Strip<T, V, VEC> x[AHEAD];
+        auto fetch = [&](int at) {
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) x[j].load(gx.at(min(at + j, end - 1)), left);
+        };
+        fetch(begin);
 #pragma unroll 1
         for (t = begin; t < end; t += AHEAD) {
-            Strip<T, V, VEC> x[AHEAD];
+            Strip<T, V, VEC> now[AHEAD];
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) x[j].load(gx.at(min(t + j, end - 1)), left);
+            for (int j = 0; j < AHEAD; ++j) now[j] = x[j];
+            if (t + AHEAD < end) fetch(t + AHEAD);
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 float y[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    win[W - 1][i] = x[j].f(i);
-                    y[i] = bias[i];
+                for (int i = 0; i < V / 2; ++i) {
+                    win[W - 1][i] = now[j].pair(i);
+                    float2 v = bias[i];
 #pragma unroll
-                    for (int k = 0; k < W; ++k) y[i] = fmaf(w[k][i], win[k][i], y[i]);
-                    if (p.silu) y[i] *= sigmoid(y[i]);
+                    for (int k = 0; k < W; ++k) v = fma2(w[k][i], win[k][i], v);
+                    if (p.silu) v = mul2(v, sigmoid2(v));
+                    y[2 * i] = v.x, y[2 * i + 1] = v.y;
 #pragma unroll
                     for (int k = 0; k < W - 1; ++k) win[k][i] = win[k + 1][i];
                 }
@@ -179,31 +225,6 @@ __global__ void __launch_bounds__(kConvThreads) conv_prompt(const ConvArgs p) {
         ++s;
         if (!p.seqs.cu) break;
     }
-}
-
-// The last W - 1 inputs of every sequence, into its state row: one thread per (sequence,
-// channel) reads them all before it writes any, so the row may be the one that was read.
-template <typename T, int W>
-__global__ void __launch_bounds__(kConvThreads) conv_states(const ConvArgs p) {
-    const int64_t i = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    const int64_t s = i / p.d;
-    cudaGridDependencySynchronize();                       // conv_prompt has read the states
-    if (s >= p.seqs.n) return;
-    const int c = (int)(i % p.d);
-    const Seq q = sequence(p.seqs, (int)s);
-    if (q.slot < 0) return;
-    const RowsOf<T> gx(p.x, p.seqs.cu ? 0 : s, c);
-    const int64_t row = q.slot * (W - 1) * p.d + c;
-    T v[W - 1];
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) {
-        const int at = q.end - (W - 1) + k;
-        v[k] = from_f32<T>(0.0f);
-        if (at >= q.start) v[k] = *reinterpret_cast<const T *>(gx.at(at));
-        else if (p.state && !q.fresh) v[k] = static_cast<const T *>(p.state)[row + (int64_t)(at - q.start + W - 1) * p.d];
-    }
-#pragma unroll
-    for (int k = 0; k < W - 1; ++k) static_cast<T *>(p.state_out)[row + (int64_t)k * p.d] = v[k];
 }
 
 // One token per sequence: the state row moves up by one.
@@ -225,13 +246,15 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
             x[k].load(reinterpret_cast<const char *>(static_cast<const T *>(p.state) + row + (int64_t)k * p.d), left);
     }
     x[W - 1].load(RowsOf<T>(p.x, b, c).at(0), left);
-    float w[W][V], y[V];
-    conv_taps<W, V>(p, c, w, y);
+    float2 w[W][V / 2], v[V / 2];
+    float y[V];
+    conv_taps<W, V>(p, c, w, v);
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
+    for (int e = 0; e < V / 2; ++e) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) y[e] = fmaf(w[k][e], x[k].f(e), y[e]);
-        if (p.silu) y[e] *= sigmoid(y[e]);
+        for (int k = 0; k < W; ++k) v[e] = fma2(w[k][e], x[k].pair(e), v[e]);
+        if (p.silu) v[e] = mul2(v[e], sigmoid2(v[e]));
+        y[2 * e] = v[e].x, y[2 * e + 1] = v[e].y;
     }
     put_strip<T, V, VEC>(const_cast<char *>(RowsOf<T>(p.y, b, c).at(0)), y, left);
 #pragma unroll
@@ -248,17 +271,17 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
 // A thread forms dpre along its run and W - 1 tokens past it (so that its dx are complete);
 // dw and db take the run's own tokens.  The runs' sums go to `part`.
 template <typename T, int W, int V, bool VEC>
-__global__ void __launch_bounds__(kConvThreads) conv_bwd(const ConvArgs p) {
+__global__ void __launch_bounds__(kConvThreads, 4) conv_bwd(const ConvArgs p) {
     const ConvSpot o = conv_spot<V>(p);
     const int left = p.d - o.c;
     const RowsOf<T> gx(p.x, o.b, o.c), go(p.dout, o.b, o.c), gdx(p.dx, o.b, o.c);
-    float w[W][V], bias[V], dw[W][V], db[V];
+    float2 w[W][V / 2], bias[V / 2], dw[W][V / 2], db[V / 2];
     conv_taps<W, V>(p, o.c, w, bias);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.0f;
+    for (int i = 0; i < V / 2; ++i) {
+        db[i] = f2(0.0f, 0.0f);
 #pragma unroll
-        for (int k = 0; k < W; ++k) dw[k][i] = 0.0f;
+        for (int k = 0; k < W; ++k) dw[k][i] = f2(0.0f, 0.0f);
     }
     int s = p.seqs.cu && o.any ? sequence_at(p.seqs, o.t0) : o.b;
     int t = o.t0;
@@ -267,7 +290,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd(const ConvArgs p) {
         const Seq q = sequence(p.seqs, s);
         const int begin = max(t, q.start), end = min(o.t1, q.end), stop = min(end + W - 1, q.end);
         if (begin < end) {
-            float win[W][V], ahead[W][V];                  // ahead[j]: dpre at t - W + 1 + j
+            float2 win[W][V / 2], ahead[W][V / 2];         // ahead[j]: dpre at t - W + 1 + j
 #pragma unroll
             for (int k = 0; k < W - 1; ++k) {
                 const int at = begin - (W - 1) + k;
@@ -275,44 +298,54 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd(const ConvArgs p) {
                 x.clear();
                 if (at >= q.start) x.load(gx.at(at), left);
 #pragma unroll
-                for (int i = 0; i < V; ++i) win[k][i] = x.f(i), ahead[k][i] = 0.0f;
+                for (int i = 0; i < V / 2; ++i) win[k][i] = x.pair(i), ahead[k][i] = f2(0.0f, 0.0f);
             }
             // token u forms dpre_u and completes dx of token u - W + 1; past `stop` dpre is zero
-            constexpr int AHEAD = 4;
-#pragma unroll 1
-            for (int u0 = begin; u0 < end + W - 1; u0 += AHEAD) {
-                Strip<T, V, VEC> x[AHEAD], g[AHEAD];
+            constexpr int AHEAD = 4;                       // tokens loaded together, a turn ahead
+            Strip<T, V, VEC> x[AHEAD], g[AHEAD];
+            auto fetch = [&](int from) {
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
-                    const int at = min(u0 + j, stop - 1);
+                    const int at = min(from + j, stop - 1);
                     x[j].load(gx.at(at), left);
                     g[j].load(go.at(at), left);
                 }
+            };
+            fetch(begin);
+#pragma unroll 1
+            for (int u0 = begin; u0 < end + W - 1; u0 += AHEAD) {
+                Strip<T, V, VEC> now_x[AHEAD], now_g[AHEAD];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) now_x[j] = x[j], now_g[j] = g[j];
+                if (u0 + AHEAD < end + W - 1) fetch(u0 + AHEAD);
 #pragma unroll
                 for (int j = 0; j < AHEAD; ++j) {
                     const int u = u0 + j;
                     float dx[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        win[W - 1][i] = x[j].f(i);
-                        float dpre = g[j].f(i);
+                    for (int i = 0; i < V / 2; ++i) {
+                        win[W - 1][i] = now_x[j].pair(i);
+                        float2 dpre = now_g[j].pair(i);
                         if (p.silu) {
-                            float pre = bias[i];
+                            float2 pre = bias[i];
 #pragma unroll
-                            for (int k = 0; k < W; ++k) pre = fmaf(w[k][i], win[k][i], pre);
-                            const float sg = sigmoid(pre);
-                            dpre *= sg * fmaf(pre, 1.0f - sg, 1.0f);
+                            for (int k = 0; k < W; ++k) pre = fma2(w[k][i], win[k][i], pre);
+                            const float2 sg = sigmoid2(pre);
+                            // silu'(v) = s (1 + v (1 - s)) = s + v s - (v s) s
+                            const float2 vs = mul2(pre, sg);
+                            dpre = mul2(dpre, fma2(f2(-vs.x, -vs.y), sg, __fadd2_rn(sg, vs)));
                         }
-                        if (u >= stop) dpre = 0.0f;
+                        if (u >= stop) dpre = f2(0.0f, 0.0f);
                         ahead[W - 1][i] = dpre;
                         if (u < end) {
-                            db[i] += dpre;
+                            db[i] = __fadd2_rn(db[i], dpre);
 #pragma unroll
-                            for (int k = 0; k < W; ++k) dw[k][i] = fmaf(dpre, win[k][i], dw[k][i]);
+                            for (int k = 0; k < W; ++k) dw[k][i] = fma2(dpre, win[k][i], dw[k][i]);
                         }
-                        dx[i] = 0.0f;
+                        float2 d = mul2(w[W - 1][i], ahead[0][i]);
 #pragma unroll
-                        for (int k = 0; k < W; ++k) dx[i] = fmaf(w[W - 1 - k][i], ahead[k][i], dx[i]);
+                        for (int k = 1; k < W; ++k) d = fma2(w[W - 1 - k][i], ahead[k][i], d);
+                        dx[2 * i] = d.x, dx[2 * i + 1] = d.y;
 #pragma unroll
                         for (int k = 0; k < W - 1; ++k) win[k][i] = win[k + 1][i], ahead[k][i] = ahead[k + 1][i];
                     }
@@ -330,8 +363,8 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd(const ConvArgs p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) sums[k * V + i][threadIdx.x] = dw[k][i];
-        sums[W * V + i][threadIdx.x] = db[i];
+        for (int k = 0; k < W; ++k) sums[k * V + i][threadIdx.x] = i % 2 ? dw[k][i / 2].y : dw[k][i / 2].x;
+        sums[W * V + i][threadIdx.x] = i % 2 ? db[i / 2].y : db[i / 2].x;
     }
     __syncthreads();
     const int64_t n = (int64_t)p.d * (W + 1);
@@ -394,28 +427,29 @@ enum ConvKind { kPrompt, kStep, kBackward };
 
 template <typename T, int W>
 vim_status conv_launch(ConvKind kind, ConvArgs &a, bool vec8, bool vec4, cudaStream_t stream) {
-    // prompts and tokens in 16-byte strips; the derivative, which keeps twice the registers
-    // per channel, in strips of 4
+    // tokens in 16-byte strips; prompts and the derivative in strips of 4 channels, whose
+    // registers leave room for twice the warps
     constexpr int V = Vec<T>::n;
-    const ConvCut cut = conv_cut(a.batch, a.L, a.d, kind == kBackward ? 4 : V);
+    const ConvCut cut = conv_cut(a.batch, a.L, a.d, kind == kStep ? V : 4);
     a.run = cut.run, a.across = cut.across;
     a.w16 = !misaligned(a.w, 16);
     const int64_t grid = kind == kStep ? ((int64_t)a.batch * cut.strips + kConvThreads - 1) / kConvThreads
                                        : cut.groups * cut.blocks;
-    if (grid > INT32_MAX) return VIM_ERR_UNSUPPORTED;
+    // states: more CTAs of the same launch, unless they go where they are read
+    const int64_t last = kind == kPrompt && a.state_out ? ((int64_t)a.seqs.n * a.d + kConvThreads - 1) / kConvThreads : 0;
+    const bool apart = a.state == a.state_out;
+    if (grid + last > INT32_MAX) return VIM_ERR_UNSUPPORTED;
+    a.ctas = (int)grid;
+    const unsigned total = (unsigned)(grid + (apart ? 0 : last));
     auto go = [&](auto kernel) {
-        if (grid > 0) kernel<<<(unsigned)grid, kConvThreads, 0, stream>>>(a);   // none: empty sequences still have states
+        if (total > 0) kernel<<<total, kConvThreads, 0, stream>>>(a);   // none: empty sequences still have states
     };
-    if (kind == kPrompt) vec8 ? go(conv_prompt<T, W, V, true>) : go(conv_prompt<T, W, V, false>);
+    if (kind == kPrompt) vec4 ? go(conv_prompt<T, W, 4, true>) : go(conv_prompt<T, W, 4, false>);
     else if (kind == kStep) vec8 ? go(conv_step<T, W, V, true>) : go(conv_step<T, W, V, false>);
     else vec4 ? go(conv_bwd<T, W, 4, true>) : go(conv_bwd<T, W, 4, false>);
     if (cudaGetLastError() != cudaSuccess) return VIM_ERR_CUDA;
-    if (kind == kPrompt && a.state_out) {
-        const int64_t n = ((int64_t)a.seqs.n * a.d + kConvThreads - 1) / kConvThreads;
-        if (n > INT32_MAX) return VIM_ERR_UNSUPPORTED;
-        if (launch_dependent(conv_states<T, W>, dim3((unsigned)n), dim3(kConvThreads), 0, stream, a) != cudaSuccess)
-            return VIM_ERR_CUDA;
-    }
+    if (apart && last > 0 && launch_dependent(conv_states<T, W>, dim3((unsigned)last), dim3(kConvThreads), 0, stream, a) != cudaSuccess)
+        return VIM_ERR_CUDA;
     return VIM_OK;
 }
 
@@ -459,11 +493,11 @@ vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, in
     a.state = seqs ? seqs->state : nullptr;
     a.state_out = seqs ? seqs->state_out : nullptr;
     a.batch = batch, a.L = L, a.d = channels, a.silu = silu != 0;
-    const int V = dt == VIM_F32 ? 4 : 8;
-    const bool vec = channels % V == 0 && conv_vec(x, batch, L, elem_size(dt), V) &&
-                     conv_vec(y, batch, L, elem_size(dt), V) && !misaligned(a.state, 16);
-    return dt == VIM_F32 ? conv_width<float>(kPrompt, a, width, vec, false, stream)
-                         : conv_width<__nv_bfloat16>(kPrompt, a, width, vec, false, stream);
+    const size_t el = elem_size(dt);
+    const bool vec = channels % 4 == 0 && conv_vec(x, batch, L, el, 4) && conv_vec(y, batch, L, el, 4) &&
+                     !misaligned(a.state, 4 * el);
+    return dt == VIM_F32 ? conv_width<float>(kPrompt, a, width, false, vec, stream)
+                         : conv_width<__nv_bfloat16>(kPrompt, a, width, false, vec, stream);
 }
 
 vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *b, int batch, int channels,
