@@ -21,11 +21,14 @@ inline bool bad_rows(const vim_rows &r, vim_dtype dt) {
     return !r.data || misaligned(r.data, elem_size(dt)) || r.batch_stride < 0 || r.row_stride < 0 ||
            r.row_stride > INT32_MAX / 4;
 }
-// an output: its rows must not overlap (rows of `width` elements)
+// an output: its rows (of `width` elements) must not overlap, whether the tokens of a batch item
+// follow one another or the batch items of a token do
 inline bool bad_out(const vim_rows &r, vim_dtype dt, int batch, int L, int width) {
     if (bad_rows(r, dt)) return true;
-    if (L > 1 && r.row_stride < width) return true;
-    return batch > 1 && r.batch_stride < (int64_t)(L - 1) * r.row_stride + width;
+    const int64_t rows = (int64_t)(L - 1) * r.row_stride + width, items = (int64_t)(batch - 1) * r.batch_stride + width;
+    const bool tokens_inside = (L <= 1 || r.row_stride >= width) && (batch <= 1 || r.batch_stride >= rows);
+    const bool items_inside = (batch <= 1 || r.batch_stride >= width) && (L <= 1 || r.row_stride >= items);
+    return !tokens_inside && !items_inside;
 }
 // whether every row of r can be read in vectors of n elements
 inline bool row_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int n) {

@@ -275,45 +275,47 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const Causa
     }
 }
 
-// dB and dC: the channel slices' parts, where there is more than one
+// The sums over what causal_bwd_main's CTAs left, in one launch: the first `param_ctas` CTAs add up
+// dA, dD and dbias over the chunks (16 partial sums per element joined in shared memory), the
+// others dB and dC over the channel slices.
 struct CausalSumArgs {
     const float *part_bc, *part_a, *part_d;
     float *dB, *dC, *dA, *dD, *dbias;
     const int *cu;
-    int n_seqs, slices, chunks, d, N;
+    int n_seqs, slices, chunks, d, N, param_ctas;
     int64_t rows;
 };
-__global__ void __launch_bounds__(256) causal_bwd_sum_bc(const CausalSumArgs p) {
-    const int64_t n = p.rows * p.N, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * n) return;
-    const int which = i >= n;
-    const int64_t k = which ? i - n : i;
-    if (p.cu) {                                            // tokens of no sequence keep what they held
-        const int64_t t = k / p.N;
-        if (t < max(p.cu[0], 0) || t >= p.cu[p.n_seqs]) return;
-    }
-    float s = 0.0f;
-    for (int x = 0; x < p.slices; ++x) s += p.part_bc[(x * 2 + which) * n + k];
-    (which ? p.dC : p.dB)[k] = s;
-}
-
-// dA, dD and dbias: sums over the chunks, 16 partial sums per element joined in shared memory
-constexpr int kSumX = 32, kSumY = 16;
-__global__ void __launch_bounds__(kSumX *kSumY) causal_bwd_sum_params(const CausalSumArgs p) {
+constexpr int kSumX = 32, kSumY = 16, kSumThreads = kSumX * kSumY;
+__global__ void __launch_bounds__(kSumThreads) causal_bwd_sums(const CausalSumArgs p) {
     __shared__ float part[kSumY][kSumX];
+    if ((int)blockIdx.x >= p.param_ctas) {
+        const int64_t n = p.rows * p.N, i = (int64_t)(blockIdx.x - p.param_ctas) * kSumThreads + threadIdx.x;
+        if (i >= 2 * n) return;
+        const int which = i >= n;
+        const int64_t k = which ? i - n : i;
+        if (p.cu) {                                        // tokens of no sequence keep what they held
+            const int64_t t = k / p.N;
+            if (t < max(p.cu[0], 0) || t >= p.cu[p.n_seqs]) return;
+        }
+        float s = 0.0f;
+        for (int x = 0; x < p.slices; ++x) s += p.part_bc[(x * 2 + which) * n + k];
+        (which ? p.dC : p.dB)[k] = s;
+        return;
+    }
+    const int tx = threadIdx.x % kSumX, ty = threadIdx.x / kSumX;
     const int64_t na = (int64_t)p.d * p.N, n = na + 2 * (int64_t)p.d;
-    const int64_t i = (int64_t)blockIdx.x * kSumX + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * kSumX + tx;
     const float *src = i < na ? p.part_a + i : p.part_d + (i - na);
     const int64_t step = i < na ? na : 2 * (int64_t)p.d;
     float s = 0.0f;
     if (i < n)
-        for (int k = threadIdx.y; k < p.chunks; k += kSumY) s += src[k * step];
-    part[threadIdx.y][threadIdx.x] = s;
+        for (int k = ty; k < p.chunks; k += kSumY) s += src[k * step];
+    part[ty][tx] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && i < n) {
+    if (ty == 0 && i < n) {
         s = 0.0f;
 #pragma unroll
-        for (int y = 0; y < kSumY; ++y) s += part[y][threadIdx.x];
+        for (int y = 0; y < kSumY; ++y) s += part[y][tx];
         if (i < na) p.dA[i] = s;
         else if (i < na + p.d) p.dD[i - na] = s;
         else p.dbias[i - na - p.d] = s;
@@ -448,11 +450,12 @@ vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const floa
     }
     if (st != VIM_OK) return st;
 
-    CausalSumArgs sum = {a.part_bc, a.part_a, a.part_d, dB, dC, dA, dD, ddelta_bias, cu_seqlens, n_seqs, pl.slices,
-                         (int)pl.chunks, d_inner, d_state, a.rows};
     const int64_t n_bc = 2 * a.rows * d_state, n_par = (int64_t)d_inner * (d_state + 2);
-    causal_bwd_sum_bc<<<(unsigned)((n_bc + 255) / 256), 256, 0, stream>>>(sum);
-    causal_bwd_sum_params<<<(unsigned)((n_par + kSumX - 1) / kSumX), dim3(kSumX, kSumY), 0, stream>>>(sum);
+    const int64_t param_ctas = (n_par + kSumX - 1) / kSumX, bc_ctas = (n_bc + kSumThreads - 1) / kSumThreads;
+    if (param_ctas + bc_ctas > INT32_MAX) return VIM_ERR_UNSUPPORTED;
+    CausalSumArgs sum = {a.part_bc, a.part_a, a.part_d, dB, dC, dA, dD, ddelta_bias, cu_seqlens, n_seqs, pl.slices,
+                         (int)pl.chunks, d_inner, d_state, (int)param_ctas, a.rows};
+    causal_bwd_sums<<<(unsigned)(param_ctas + bc_ctas), kSumThreads, 0, stream>>>(sum);
     return cudaGetLastError() == cudaSuccess ? VIM_OK : VIM_ERR_CUDA;
 }
 

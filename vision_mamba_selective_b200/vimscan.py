@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -749,8 +750,8 @@ lib.clip_grad_norm_workspace_bytes.argtypes = [_i]
 lib.clip_grad_norm_workspace_bytes.restype = _sz
 
 # The structs of the causal entry points (vim_scan_io and the like, vim_sequences, vim_tensor)
-# hold nothing but 64-bit values, so they are handed over as arrays of those.
-_i64x = {n: _i64 * n for n in (6, 7, 9, 18, 27)}
+# hold nothing but 64-bit values, so they are handed over as packed bytes of those.
+_i64x = {n: struct.Struct(f"{n}q").pack for n in (6, 7, 9, 18, 27)}
 
 
 def _check_ref(where, ref):
@@ -891,7 +892,7 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
     dt = _dtype_code(u)
     made = None
     if y is None:
-        y = made = torch.empty(act, dtype=io, device=u.device)
+        y = made = torch.empty_like(u)
     rows = _i64x[18](
         *_rows(where, "u", u, io, act, dev, packed), *_rows(where, "delta", delta, io, act, dev, packed),
         *_rows(where, "z", z, io, act, dev, packed), *_rows(where, "B", B, io, bc, dev, packed),
@@ -924,7 +925,7 @@ def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=No
     dt = _dtype_code(u)
     made = None
     if y is None:
-        y = made = torch.empty(act, dtype=io, device=u.device)
+        y = made = torch.empty_like(u)
     rows = _i64x[18](
         *_rows(where, "u", u, io, act, dev, False), *_rows(where, "delta", delta, io, act, dev, False),
         *_rows(where, "z", z, io, act, dev, False), *_rows(where, "B", B, io, bc, dev, False),
@@ -963,11 +964,11 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
     made = ()
     if out is None:
-        fill = torch.zeros if packed else torch.empty
-        acts = lambda: fill(act, dtype=io, device=u.device)
-        f = lambda *shape, of=torch.empty: of(shape, dtype=f32, device=u.device)
-        out = dict(du=acts(), ddelta=acts(), dz=None if z is None else acts(), dB=f(*bc, of=fill), dC=f(*bc, of=fill),
-                   dA=f(Di, N), dD=f(Di), ddelta_bias=f(Di))
+        like = torch.zeros_like if packed else torch.empty_like
+        f = u.new_zeros if packed else u.new_empty
+        out = dict(du=like(u), ddelta=like(u), dz=None if z is None else like(u), dB=f(bc, dtype=f32), dC=f(bc, dtype=f32),
+                   dA=u.new_empty((Di, N), dtype=f32), dD=u.new_empty(Di, dtype=f32),
+                   ddelta_bias=u.new_empty(Di, dtype=f32))
         made = tuple(out.values())
     elif (z is None) != (out["dz"] is None):
         raise ValueError(f"{where}: out['dz'] must be given exactly when z is")
@@ -1013,7 +1014,7 @@ def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=No
     io, f32, act = x.dtype, torch.float32, x.shape
     made = None
     if y is None:
-        y = made = torch.empty(act, dtype=io, device=x.device)
+        y = made = torch.empty_like(x)
     dt = _dtype_code(x)
     rows = _i64x[6](*_rows(where, "x", x, io, act, dev, packed), *_rows(where, "y", y, io, act, dev, packed))
     pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
@@ -1040,7 +1041,7 @@ def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, slots=None, y
     io, f32, act = x.dtype, torch.float32, x.shape
     made = None
     if y is None:
-        y = made = torch.empty(act, dtype=io, device=x.device)
+        y = made = torch.empty_like(x)
     dt = _dtype_code(x)
     rows = _i64x[6](*_rows(where, "x", x, io, act, dev, False), *_rows(where, "y", y, io, act, dev, False))
     pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
@@ -1072,9 +1073,8 @@ def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None
     io, f32, act = x.dtype, torch.float32, x.shape
     made = ()
     if out is None:
-        out = dict(dx=(torch.zeros if packed else torch.empty)(act, dtype=io, device=x.device),
-                   dw=torch.empty((Ch, W), dtype=f32, device=x.device),
-                   db=None if b is None else torch.empty((Ch,), dtype=f32, device=x.device))
+        out = dict(dx=(torch.zeros_like if packed else torch.empty_like)(x), dw=x.new_empty((Ch, W), dtype=f32),
+                   db=None if b is None else x.new_empty(Ch, dtype=f32))
         made = tuple(out.values())
     elif (b is None) != (out["db"] is None):
         raise ValueError(f"{where}: out['db'] must be given exactly when b is")
@@ -1132,23 +1132,31 @@ def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stre
     if not max_norm >= 0:
         raise ValueError(f"{where}: max_norm must be >= 0, got {max_norm}")
     dev = torch.cuda.current_device()
-    table = []
-    for i, (t, o) in enumerate(zip(src, dst)):
-        # one pass of cheap checks; what is wrong is worked out only where one fails
-        if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()
-                and t.dtype in _CLIP_TYPES):
+    try:
+        # cheap checks of all at once; what is wrong is worked out only where one fails
+        codes = [_CLIP_TYPES.get(t.dtype) for t in src]
+        good = None not in codes and all([t.get_device() == dev and t.is_contiguous() for t in src])
+        at = [t.data_ptr() for t in src]
+        to = at
+        if out is not None:
+            good = good and all([o.get_device() == dev and o.is_contiguous() and o.dtype == t.dtype and o.shape == t.shape
+                                 for t, o in zip(src, dst)])
+            to = [o.data_ptr() for o in dst]
+        table = [v for row in zip(at, to, [t.numel() for t in src], codes) for v in row] if good else None
+    except (AttributeError, RuntimeError):
+        table = None
+    if table is None:
+        for i, (t, o) in enumerate(zip(src, dst)):
             _refuse_gradient(where, f"grads[{i}]", t, dev)
-        if o is not t and not (isinstance(o, torch.Tensor) and o.get_device() == dev and o.is_contiguous()
-                               and o.dtype == t.dtype and o.shape == t.shape):
             _refuse_gradient(where, f"out[{i}]", o, dev)
-            raise ValueError(f"{where}: out[{i}] must be {t.dtype} of shape {tuple(t.shape)}, got {o.dtype} of "
-                             f"{tuple(o.shape)}")
-        at = t.data_ptr()
-        table += (at, at if o is t else o.data_ptr(), t.numel(), _CLIP_TYPES[t.dtype])
+            if o.dtype != t.dtype or o.shape != t.shape:
+                raise ValueError(f"{where}: out[{i}] must be {t.dtype} of shape {tuple(t.shape)}, got {o.dtype} of "
+                                 f"{tuple(o.shape)}")
+        raise TypeError(f"{where}: grads and out must be tensors with storage")
     device = torch.device("cuda", dev)
     made = []
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=device)
+        norm = src[0].new_empty(1, dtype=torch.float32) if src else torch.empty(1, dtype=torch.float32, device=device)
         made.append(norm)
     elif not isinstance(norm, torch.Tensor) or norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
         raise ValueError(f"{where}: norm must be one float32 element on cuda:{dev}")
@@ -1157,7 +1165,7 @@ def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stre
     ws, ws_bytes = _workspace(clip_grad_norm_workspace_bytes(n), workspace, device)
     if given is None:
         made.append(ws)
-    st = lib.clip_grad_norm((_i64 * max(1, len(table)))(*table), n, max_norm, norm.data_ptr(), ws.data_ptr(), ws_bytes,
+    st = lib.clip_grad_norm(struct.pack(f"{4 * n}q", *table), n, max_norm, norm.data_ptr(), ws.data_ptr(), ws_bytes,
                             _launch_stream(dev, stream, *made))
     if st != VIM_OK:
         raise VimScanError(st, where)
