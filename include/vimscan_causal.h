@@ -65,13 +65,16 @@ typedef struct {
  *   y_t = (C_t . h_t + D u_t) * silu(z_t)
  *   u, delta, z, y : rows of d_inner channels (dt); z.data may be NULL (no gate).
  *   B, C           : rows of d_state (dt), shared by all channels of a token.
- *   A              : [d_inner, d_state] fp32, any values, 16-byte aligned; D, delta_bias :
- *                    [d_inner] fp32.
+ *   A              : [d_inner, d_state] fp32, 16-byte aligned, meant to be <= 0 (of any
+ *                    values; with A > 0 the decays of 8 tokens together must stay finite);
+ *                    D, delta_bias : [d_inner] fp32.
  *   seqs           : NULL: batch rows, no states.  States are fp32 [n_slots, d_inner,
  *                    d_state], 16-byte aligned.
  *   ckpt           : NULL, or fp32 causal_ckpt_bytes(batch, L, d_inner, d_state) bytes,
  *                    16-byte aligned: the state entering every 8th token of a row,
- *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd.
+ *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd.  Not
+ *                    together with initial states (VIM_ERR_INVALID_ARG): the derivative
+ *                    starts every sequence from zeros.
  * One launch, no workspace.
  */
 typedef struct {
@@ -121,7 +124,7 @@ size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, in
  * over the past only):
  *   pre[b,t,c] = b[c] + sum_k w[c][k] x[b, t - width + 1 + k, c],   k = 0 .. width - 1
  *   y = silu(pre) where `silu` is non-zero, else pre
- *   x, y   : rows of `channels` (dt); y must not overlap x.
+ *   x, y   : rows of `channels` (dt); y must not overlap x (the same address is refused).
  *   w      : [channels, width] fp32, width 2, 3 or 4 (the newest tap last); b : [channels]
  *            fp32 or NULL.
  *   seqs   : states are [n_slots, width - 1, channels] (dt), aligned to their elements: the

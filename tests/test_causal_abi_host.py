@@ -30,10 +30,10 @@ def i64(*values):
 
 
 def rows(n, batch=600, row=64, **other):
-    """n vim_rows of FAKE data; other: index -> (data, batch stride, row stride)."""
+    """n vim_rows of FAKE data, far from one another; other: index -> (data, batch stride, row stride)."""
     v = []
     for i in range(n):
-        v += other.get(f"r{i}", (FAKE, batch, row))
+        v += other.get(f"r{i}", (FAKE + (i << 32), batch, row))
     return i64(*v)
 
 
@@ -83,6 +83,8 @@ def test_scan_refusals(vs):
     assert scan(vs, dt=2) == bad
     assert scan(vs, N=3) == uns and scan(vs, N=32) == uns
     assert scan(vs, ckpt=FAKE + 4) == bad
+    assert scan(vs, ckpt=FAKE, seqs=i64(0, 2, FAKE, FAKE, 0, 2, 0)) == bad         # kept states start from zeros
+    assert scan(vs, L=2**31 - 8) == uns and scan(vs, d=2**31 - 8) == uns           # counted in ints with tiles
     # sequences: cu, n, state, state_out, slots, n_slots, fresh
     assert scan(vs, seqs=i64(0, 3, 0, 0, 0, 0, 0)) == bad                          # not one per batch row
     assert scan(vs, seqs=i64(FAKE, 3, 0, 0, 0, 0, 0)) == bad                       # packed, batch 2
@@ -136,6 +138,9 @@ def test_scan_bwd_refusals(vs):
     assert scan_bwd(vs, rows(9, r8=(0, 0, 0))) == bad                              # z without dz
     for i in (6, 7, 8):
         assert scan_bwd(vs, rows(9, **{f"r{i}": (FAKE, 600, 63)})) == bad, i
+    for o in (6, 7, 8):
+        for i in (0, 1, 2, 5):                                                     # an output over an input
+            assert scan_bwd(vs, rows(9, **{f"r{o}": (FAKE, 600, 64), f"r{i}": (FAKE, 600, 64)})) == bad
     assert scan_bwd(vs, grads=None) == bad and scan_bwd(vs, grads=FAKE + 2) == bad
     assert scan_bwd(vs, ckpt=FAKE + 8) == bad
     assert scan_bwd(vs, cu=FAKE, n=2) == bad                                       # packed, batch 2
@@ -158,6 +163,8 @@ def test_conv_refusals(vs):
         assert conv(vs, rows(2, **{f"r{i}": (0, 600, 64)})) == bad
         assert conv(vs, rows(2, **{f"r{i}": (FAKE + 1, 600, 64)})) == bad
     assert conv(vs, rows(2, r1=(FAKE, 600, 60))) == bad
+    assert conv(vs, rows(2, r1=(FAKE, 600, 64), r0=(FAKE, 600, 64))) == bad        # in place
+    assert conv(vs, L=2**31 - 8) == uns
     assert conv(vs, w=None) == bad and conv(vs, w=FAKE + 2) == bad and conv(vs, b=FAKE + 1) == bad
     assert conv(vs, W=1) == uns and conv(vs, W=5) == uns
     assert conv(vs, dt=9) == bad and conv(vs, L=-1) == bad
@@ -177,6 +184,8 @@ def test_conv_bwd_refusals(vs):
     for i in range(3):
         assert bwd(rows(3, **{f"r{i}": (0, 600, 64)})) == bad
     assert bwd(rows(3, r2=(FAKE, 600, 1))) == bad
+    for i in range(2):                                                             # dx over x or dout
+        assert bwd(rows(3, r2=(FAKE, 600, 64), **{f"r{i}": (FAKE, 600, 64)})) == bad
     assert bwd(dw=None) == bad and bwd(b=None) == bad and bwd(db=FAKE + 2) == bad
     assert bwd(cu=FAKE, n=2) == bad
     assert bwd(W=7) == vs.VIM_ERR_UNSUPPORTED

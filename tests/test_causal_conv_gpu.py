@@ -240,6 +240,23 @@ def test_stream_graph_and_repeats(vs):
         assert torch.equal(y, y3) and all(torch.equal(g[k], g3[k]) for k in g)
 
 
+def test_time_major_and_far_rows(vs):
+    """[L, batch, channels] in memory; rows 2^27 elements apart (element offsets to 2^32)."""
+    x, w, b = inputs((3, 40), 24, 4, F32, 6)
+    want, _ = causal_ref.conv(x, w, b)
+    y = vs.causal_conv(x.transpose(0, 1).contiguous().cuda().transpose(0, 1), cuda(w), cuda(b))
+    close(y, want, TOL[F32])
+    L, d = 34, 16
+    x, w, b = inputs((1, L), d, 4, BF, 7)
+    base = torch.empty((L, 1 << 27), dtype=BF, device="cuda")
+    far = base[:, :d]
+    far.copy_(x[0].cuda())
+    y = base[:, 64:64 + d][None]
+    vs.causal_conv(far[None], cuda(w), cuda(b), y=y)
+    want, _ = causal_ref.conv(x, w, b)
+    close(y, want, TOL[BF])
+
+
 def test_refusals(vs):
     x, w, b = (cuda(t) for t in inputs((2, 10), 32, 4, F32, 1))
     state = torch.zeros((2, 3, 32), device="cuda")
@@ -256,6 +273,7 @@ def test_refusals(vs):
         (ValueError, lambda: vs.causal_conv(x[0], w, b)),
         (vs.VimScanError, lambda: vs.causal_conv(x, torch.zeros((32, 5), device="cuda"), b)),
         (vs.VimScanError, lambda: vs.causal_conv(x, torch.zeros((32, 1), device="cuda"), b)),
+        (vs.VimScanError, lambda: vs.causal_conv(x, w, b, y=x)),                          # in place
         (ValueError, lambda: vs.causal_conv_step(x, w, b, state)),
         (ValueError, lambda: vs.causal_conv_step(x[:, 0], w, b, None)),
         (ValueError, lambda: vs.causal_conv_bwd(x, w, b, dout[:, :9])),

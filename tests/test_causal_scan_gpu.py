@@ -316,6 +316,7 @@ def test_refusals(vs):
         (TypeError, lambda: vs.causal_scan(*a, state=state, slots=torch.zeros(2, dtype=torch.int64, device="cuda"))),
         (ValueError, lambda: vs.causal_scan(*a, state=state, slots=torch.zeros(3, dtype=torch.int32, device="cuda"))),
         (ValueError, lambda: vs.causal_scan(*a, ckpt=torch.zeros((2, 1, 32, 16), device="cuda"))),
+        (ValueError, lambda: vs.causal_scan(*a, state=state, ckpt=torch.zeros((2, 2, 32, 16), device="cuda"))),
         (ValueError, lambda: vs.causal_scan(*a, y=torch.zeros((2, 10, 31), device="cuda"))),
         (vs.VimScanError, lambda: vs.causal_scan(*a, y=torch.zeros((1, 10, 32), device="cuda").expand(2, 10, 32))),
         (ValueError, lambda: vs.causal_scan_step(*a, state)),
@@ -326,6 +327,56 @@ def test_refusals(vs):
             call()
             raise AssertionError(f"call {i} was not refused")
     assert (state == 0).all()
+
+
+def test_time_major(vs):
+    """Tensors that lie [L, batch, channels] in memory, outputs among them."""
+    p = inputs((3, 40), 24, 16, F32, 6)
+    a = cuda({k: v.transpose(0, 1).contiguous().transpose(0, 1) if v.dim() == 3 else v for k, v in p.items()})
+    assert not a[0].is_contiguous()
+    y = vs.causal_scan(*a)
+    want, _ = ref(p)
+    close(y, want, Y_TOL[F32])
+
+
+def test_long_sequence(vs):
+    """20000 tokens, few channels: many handovers, slow decays."""
+    p = inputs((1, 20000), 4, 16, F32, 12)
+    state = torch.empty((1, 4, 16), device="cuda")
+    y = vs.causal_scan(*cuda(p), state_out=state)
+    want, last = ref(p)
+    close(y, want, Y_TOL[F32])
+    close(state, last, STATE_TOL)
+
+
+def test_offsets_past_32_bits(vs):
+    """Rows 2^27 elements apart (element offsets to 2^32) and a state cache of 2.3e9 elements."""
+    L, d, N, far = 34, 16, 16, 1 << 27
+    p = inputs((1, L), d, N, BF, 4)
+    base = torch.empty((L, far), dtype=BF, device="cuda")
+    args = cuda(p)
+    for i, at in ((0, 0), (1, 64), (2, 128)):
+        view = base[:, at:at + d]
+        view.copy_(args[i][0])
+        args[i] = view[None]
+    y = base[:, 256:256 + d][None]
+    vs.causal_scan(*args, y=y)
+    want, _ = ref(p)
+    close(y, want, Y_TOL[BF])
+    del base, y, args
+    slots, d = 70000, 2048
+    q = inputs((2, 1), d, N, BF, 5)
+    want, last = ref(q)
+    u, delta, z, B, C, A, D, bias = cuda(q)
+    cache = torch.empty((slots, d, N), device="cuda")
+    rows = torch.tensor([slots - 1, 3], dtype=torch.int32, device="cuda")
+    cache[rows.long()] = 0
+    y = vs.causal_scan_step(u[:, 0], delta[:, 0], z[:, 0], B[:, 0], C[:, 0], A, D, bias, cache, slots=rows)
+    close(y, want[:, 0], Y_TOL[BF])
+    close(cache[rows.long()], last, STATE_TOL)
+    cache[rows.long()] = 0
+    vs.causal_scan(u, delta, z, B, C, A, D, bias, state=cache, slots=rows)
+    close(cache[rows.long()], last, STATE_TOL)
 
 
 def test_empty(vs):

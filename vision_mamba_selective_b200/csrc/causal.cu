@@ -152,6 +152,7 @@ vim_status causal_scan(const vim_scan_io *io, const float *A, const float *D, co
     std::memset(&a, 0, sizeof(a));
     st = make_seqs(seqs, batch, L, 16, &a.seqs);
     if (st != VIM_OK) return st;
+    if (ckpt && seqs && seqs->state) return VIM_ERR_INVALID_ARG;   // the derivative starts every sequence from zeros
     if (a.seqs.n == 0 || d_inner == 0) return VIM_OK;
     if (L > 0) {
         st = check_scan(u, delta, z, B, C, A, D, delta_bias, dt);

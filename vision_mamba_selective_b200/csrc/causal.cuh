@@ -37,6 +37,7 @@ inline bool row_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int n
 }
 inline vim_status check_sizes(int batch, int L, int channels, vim_dtype dt) {
     if (batch < 0 || L < 0 || channels < 0 || (dt != VIM_F32 && dt != VIM_BF16)) return VIM_ERR_INVALID_ARG;
+    if (L > INT32_MAX - 1024 || channels > INT32_MAX - 1024) return VIM_ERR_UNSUPPORTED;   // tiles past the end are counted in ints
     return VIM_OK;
 }
 

@@ -408,6 +408,10 @@ vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const floa
     if (!A || !D || !delta_bias || misaligned(A, 16) || misaligned(D, 4) || misaligned(delta_bias, 4))
         return VIM_ERR_INVALID_ARG;
     if (bad_out(du, dt, batch, L, d_inner) || bad_out(ddelta, dt, batch, L, d_inner)) return VIM_ERR_INVALID_ARG;
+    // (an output over an input: other warps may still have to read it)
+    for (const vim_rows *o : {&du, &ddelta, &dz})
+        for (const vim_rows *i : {&u, &delta, &z, &dout})
+            if (o->data && o->data == i->data) return VIM_ERR_INVALID_ARG;
     if (!z.data != !dz.data || (z.data && bad_out(dz, dt, batch, L, d_inner))) return VIM_ERR_INVALID_ARG;
     if (!dB || !dC || misaligned(dB, 4) || misaligned(dC, 4) || misaligned(ckpt, 16)) return VIM_ERR_INVALID_ARG;
     const CausalBwdPlan pl = causal_bwd_plan(batch, L, d_inner, d_state, ckpt != nullptr);

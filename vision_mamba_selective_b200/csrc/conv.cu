@@ -488,7 +488,8 @@ vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, in
     st = make_seqs(seqs, batch, L, elem_size(dt), &a.seqs);
     if (st != VIM_OK) return st;
     if (a.seqs.n == 0 || channels == 0) return VIM_OK;
-    if (L > 0 && (bad_rows(x, dt) || bad_out(y, dt, batch, L, channels))) return VIM_ERR_INVALID_ARG;
+    // (in place, tokens would be overwritten before their successors have read them)
+    if (L > 0 && (bad_rows(x, dt) || bad_out(y, dt, batch, L, channels) || y.data == x.data)) return VIM_ERR_INVALID_ARG;
     a.x = x, a.y = y, a.w = w, a.b = b;
     a.state = seqs ? seqs->state : nullptr;
     a.state_out = seqs ? seqs->state_out : nullptr;
@@ -555,7 +556,9 @@ vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const floa
                         (!db || cudaMemsetAsync(db, 0, n, stream) == cudaSuccess);
         return ok ? VIM_OK : VIM_ERR_CUDA;
     }
-    if (bad_rows(x, dt) || bad_rows(dout, dt) || bad_out(dx, dt, batch, L, channels)) return VIM_ERR_INVALID_ARG;
+    if (bad_rows(x, dt) || bad_rows(dout, dt) || bad_out(dx, dt, batch, L, channels) || dx.data == x.data ||
+        dx.data == dout.data)
+        return VIM_ERR_INVALID_ARG;
     const size_t need = causal_conv_bwd_workspace_bytes(batch, L, channels, width);
     if (!workspace || workspace_bytes < need || misaligned(workspace, kAlign)) return VIM_ERR_WORKSPACE;
     a.x = x, a.dout = dout, a.dx = dx, a.w = w, a.b = b;

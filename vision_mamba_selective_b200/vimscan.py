@@ -880,10 +880,13 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
     sequence order by default; a slot outside the cache marks a padding entry, which is
     skipped.  ``fresh`` (bool, one per sequence) starts a sequence from zeros.
 
-    ``ckpt``, fp32 of causal_ckpt_shape(...), receives the states causal_scan_bwd takes.
+    ``ckpt``, fp32 of causal_ckpt_shape(...), receives the states causal_scan_bwd takes (not
+    together with ``state``: the derivative starts every sequence from zeros).
     Returns y, shaped like u.
     """
     where = "causal_scan"
+    if ckpt is not None and state is not None:
+        raise ValueError(f"{where}: ckpt is for sequences that start from zeros; give state_out alone")
     dev = _check_ref(where, u)
     batch, L, Di = _token_shape(where, u, "u", cu_seqlens)
     N = B.shape[-1]
