@@ -50,9 +50,12 @@ __device__ __forceinline__ float reduce_channels(float (&v)[n], int cl) {
 // time, the chunk's segments of 8 tokens from the last to the first.  Per segment a warp
 // runs the recurrence forward from its kept state, holding the decays and m_t in
 // registers (one exponential per token, channel and state), then the adjoint backward.
-// Bound by issue: 24 packed operations on a lane's 4 states per token, against about 100
-// instructions with the sums over lanes (dB and dC over channels, three sums over states)
-// and the per-token functions.
+// Bound by latency and issue: 960 instructions per 64 token-channels, 192 of them the packed
+// arithmetic, 250 the selects and shuffles of the sums (dB and dC over channels, three
+// sums over states), at half an instruction a clock and scheduler.  Two CTAs an SM, with
+// room for all of a segment in registers: at three the compiler spills 250 bytes a thread
+// (8 x 4097 tokens x 384 channels, N = 16, bf16: 320 us, 510 with the spills; with m_t in
+// shared memory and loads held back, so that three fit, 330).
 template <typename T, int N, int NL, bool PACKED>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const CausalBwdArgs p) {
     constexpr int LPC = N / NL, CH = 32 / LPC, NP = NL / 2, EPL = kSeg / LPC, NV = 2 * NL;

@@ -21,9 +21,9 @@
 //   2. runs the segment from h = 0, multiplying up its decays: with P_t the product so far,
 //      h_t = P_t h_in + hz_t, and C_t . h_t = C_t . hz_t + (C_t P_t) . h_in; C_t P_t and the
 //      first sum stay in registers, all of it without knowing h_in;
-//   3. takes h_in from the warp before it and hands h_out on to the next (two multiply-adds
-//      between a named barrier's wait and its arrival: the only serial part), and
-//   4. adds (C_t P_t) . h_in to the sums, two multiply-adds per pair of states and token.
+//   3. takes h_in from the warp before it and hands h_out on to the next (a multiply-add per
+//      pair of states between a named barrier's wait and its arrival: the only serial part),
+//   4. adds (C_t P_t) . h_in to the sums, a multiply-add per pair of states and token.
 // A channel's N states lie on N / NL lanes, NL a lane in f32x2 pairs; the partial sums of
 // C . h are reduced over these lanes so that each ends with the y of its own tokens, gates
 // them and stores them.  Lanes of one state group are neighbours: a 16-byte read of B or C
@@ -33,7 +33,11 @@
 // outside the sequence get Delta = 0 and Delta u = 0, which leave the state as it is.
 //
 // The adjoint, and the states kept for the derivative, are wanted only at segment borders:
-// these modes end with step 3.
+// these modes end with step 3, and are bound by the handovers (about 200 clocks each).
+//
+// Measured at N = 16, bf16 (the special-function floor in parentheses): 8192 packed tokens x
+// 2048 channels 149 us (74), 4 x 16385 x 384 334 us (111), 8 x 4097 x 384 with kept states
+// 146 us (55); 0.65 instructions a clock and scheduler, shared-memory pipe at 67%.
 #pragma once
 
 #include "causal.cuh"

@@ -3,9 +3,12 @@
 //
 //   pre_t = b + sum_(k < W) w_k x_(t - W + 1 + k),   y_t = silu(pre_t) or pre_t
 //
-// All of it is bound by memory traffic (two elements per token-channel forward, three
-// backward), so every thread walks down the tokens of a few neighbouring channels with the
-// last W - 1 inputs in registers: each input is read once.
+// The traffic is two elements per token-channel forward, three backward, so every thread walks
+// down the tokens of four neighbouring channels with the last W - 1 inputs in registers: each
+// input is read once, a turn of 8 (4) tokens ahead.  At bf16 the SiLU is then as long as the
+// traffic: two special-function operations an element, 7.5 us for 8192 x 2048 (10.3 us of
+// traffic, 20.5 us measured, by latency: 14 warps an SM; strips of 8 channels, twice the
+// warps with shorter runs: 22 to 26 us).  8 x 4097 x 384: 16 us forward, 29 us backward.
 #include "causal.cuh"
 
 #include <algorithm>
