@@ -99,6 +99,7 @@ PACKED = [
     ([64, 64], 16, 16, F32, 0, 70),
     ([60, 8, 90], 16, 4, F32, 68, 3),
     ([17] * 12, 64, 2, BF, 0, 1),
+    ([9, 0, 20, 3], 4100, 16, F32, 0, 2),            # enough channels for eight states a lane
 ]
 
 

@@ -123,6 +123,9 @@ PACKED = [
     ([0, 0], 16, 4, F32, 0, 3),
     ([17] * 12, 64, 2, BF, 0, 1),
     ([200, 3, 77], 3200, 16, BF, 0, 0),
+    ([40, 3, 77, 0, 9, 9], 3200, 16, F32, 2, 1),     # enough channels for eight states a lane
+    ([(i * 7) % 5 for i in range(64)], 24, 16, F32, 0, 0),
+    ([(i * 7) % 5 for i in range(70)], 24, 8, BF, 3, 0),   # more sequences than are sorted by length
 ]
 
 

@@ -69,6 +69,7 @@ enum CausalMode {
 namespace {
 
 constexpr int kSeg = 8;             // most tokens of a segment
+constexpr int kMostRanked = 64;     // packed sequences that are walked in the order of their lengths
 constexpr int kPassWarps = 8;       // most warps of a CTA: one named barrier each
 static_assert(kCkEvery == kSeg && kAdjEvery % kSeg == 0, "kept states lie at segment borders");
 
@@ -117,8 +118,28 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(
     S &sm = reinterpret_cast<S *>(pass_smem)[w];
     S &next = reinterpret_cast<S *>(pass_smem)[w + 1 == W ? 0 : w + 1];
 
-    const int blocks = (p.d + CH - 1) / CH;
-    const int s = blockIdx.x / blocks, c0 = (blockIdx.x % blocks) * CH;
+    const int blocks = (p.d + CH - 1) / CH, c0 = (blockIdx.x % blocks) * CH;
+    int s = blockIdx.x / blocks;
+    if (p.seqs.cu && p.seqs.n > 1 && p.seqs.n <= kMostRanked) {
+        // packed sequences from the longest to the shortest, so that no long one starts last
+        // (8192 tokens x 2048 channels in 11 and 60 sequences, mean of 8 draws: 166 -> 147 and
+        // 202 -> 175 us): CTA group k takes the sequence that k others are longer than (or as
+        // long, and before)
+        int *const found = reinterpret_cast<int *>(pass_smem);
+        for (int i = threadIdx.x; i < p.seqs.n; i += blockDim.x) {
+            const int length = p.seqs.cu[i + 1] - p.seqs.cu[i];
+            int rank = 0, before = p.seqs.cu[0];
+            for (int j = 0; j < p.seqs.n; ++j) {
+                const int after = p.seqs.cu[j + 1], other = after - before;
+                rank += other > length || (other == length && j < i);
+                before = after;
+            }
+            if (rank == s) *found = i;
+        }
+        __syncthreads();
+        s = *found;
+        __syncthreads();
+    }
     const Seq seq = sequence(p.seqs, s);
     const int64_t b = p.seqs.cu ? 0 : s;
     const int q = lane / CH, cl = lane % CH;
@@ -297,21 +318,22 @@ inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 // How a call is cut: states a lane holds, tokens of a segment, warps of a CTA.
 //   - Eight states and segments of 4 (16 channels a warp, 32-byte rows at bf16) need fewer
 //     loads, shuffles and selects per token-channel than four and segments of 8, but half
-//     the CTAs and twice the handovers per token: better from 8192 channels on (11 packed
-//     sequences x 2048 channels: 147 us against 164; 4 x 2048 tokens x 4096: 279 and 301),
-//     worse below (1 x 4096 tokens x 2048 channels: 113 and 92).
+//     the CTAs and twice the handovers per token: better from 8192 channels on (4 x 2048
+//     tokens x 4096: 279 us against 301), worse below (1 x 4096 tokens x 2048 channels: 113
+//     and 92).  Packed, where one sequence may hold most of the tokens, from 16384 on (8192
+//     tokens in 11 sequences x 2048 channels: 147 and 168; in 4: 227 and 164; 4000 tokens in
+//     20 x 768: 45 and 38).
 //   - Eight warps hide the handover best; four waste less where sequences are short
 //     (64 x 16 tokens x 4096 channels: 68 us against 115; 16 x 200 x 2048: 61 and 68; 64 x
-//     500 x 768: 203 and 209; the 11 packed sequences above, 745 tokens on average: 162 and
-//     147), and where the CTAs then run in one round instead of a full and a partial one
+//     500 x 768: 203 and 209; 11 packed sequences of 745 tokens on average: 162 and 147), and where the CTAs then run in one round instead of a full and a partial one
 //     (8 x 4097 tokens x 384 channels: 141 and 151).  A row has no work for more warps than
 //     segments.
 struct PassPlan {
     int states, seg, warps;
 };
-inline PassPlan pass_plan(int mode, int N, int64_t channels, int64_t tokens_per_seq, int L) {
+inline PassPlan pass_plan(int mode, int N, int64_t channels, bool packed, int64_t tokens_per_seq, int L) {
     PassPlan pl;
-    const bool thick = N == 16 && channels >= 8192;
+    const bool thick = N == 16 && channels >= (packed ? 16384 : 8192);
     pl.states = thick ? 8 : N >= 8 ? 4 : 2;
     pl.seg = thick ? 4 : kSeg;
     const int64_t ctas = channels * N / pl.states / 32, slots = 148 * pass_ctas(mode);
