@@ -69,6 +69,9 @@ CASES = [
     (1, 150, 1, 16, F32, True, False),
     (2, 40, 300, 8, BF, False, False),
     (1, 129, 200, 4, F32, True, True),
+    (3, 90, 264, 16, F32, True, True),         # segments of 16, 4 lanes a channel
+    (1, 150, 700, 16, BF, True, False),
+    (2, 145, 600, 16, F32, True, False),       # segments of 8
     (2, 21, 4100, 16, F32, True, False),       # 8200 channels: eight states a lane
     (1, 70, 8200, 16, BF, True, True),
 ]

@@ -92,6 +92,10 @@ BATCH = [
     (1, 130, 2400, 16, BF, True, False),       # 8 lanes a channel
     (5, 70, 2000, 16, F32, True, False),       # 4 lanes a channel
     (8, 40, 1300, 8, BF, True, False),         # N = 8, 4 lanes a channel
+    (1, 300, 592, 16, BF, True, True),         # 8 lanes a channel, segments of 16
+    (2, 97, 297, 16, F32, True, False),        # 4 lanes a channel, segments of 16
+    (1, 300, 1184, 16, BF, True, True),
+    (3, 90, 395, 16, F32, True, True),         # segments of 8
 ]
 
 
@@ -123,6 +127,8 @@ PACKED = [
     ([0, 0], 16, 4, F32, 0, 3),
     ([17] * 12, 64, 2, BF, 0, 1),
     ([200, 3, 77], 3200, 16, BF, 0, 0),
+    ([150, 0, 3, 77, 16], 200, 16, F32, 5, 1),       # segments of 16, 4 lanes a channel
+    ([150, 0, 3, 77, 16], 300, 16, BF, 5, 1),        # segments of 8
     ([40, 3, 77, 0, 9, 9], 3200, 16, F32, 2, 1),     # enough channels for eight states a lane
     ([(i * 7) % 5 for i in range(64)], 24, 16, F32, 0, 0),
     ([(i * 7) % 5 for i in range(70)], 24, 8, BF, 3, 0),   # more sequences than are sorted by length

@@ -204,9 +204,20 @@ struct RowsOf {
         if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const uint32_t *>(at(t)) + i);
         else return __ldg(reinterpret_cast<const uint16_t *>(at(t)) + i);
     }
-    // n 32-bit words of elements: at once, aligned to their size, or element by element
+    // n 32-bit words of elements: at once, aligned to their size or to four elements, or
+    // element by element
     template <int n> __device__ __forceinline__ void words(int t, uint32_t (&v)[n]) const {
-        if constexpr (n == 4) {
+        if constexpr (n > (int)sizeof(T)) {                // eight elements
+            if constexpr (sizeof(T) == 4) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at(t)));
+                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at(t)) + 1);
+                v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+            } else {
+                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at(t)));
+                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(at(t)) + 1);
+                v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+            }
+        } else if constexpr (n == 4) {
             const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at(t)));
             v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         } else if constexpr (n == 2) {

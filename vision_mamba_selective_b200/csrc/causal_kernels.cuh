@@ -16,7 +16,7 @@
 // on its scheduler a warp issues an instruction every four clocks.
 //
 // The walk is shared by the W warps of a CTA, which all hold the same few channels and
-// take segments of SEG tokens (8, or 4) in turn.  For its segment a warp
+// take segments of SEG tokens (8; 16 or 4) in turn.  For its segment a warp
 //   1. forms Delta and Delta u of its tokens, each lane its share (exchanged by shuffles);
 //   2. runs the segment from h = 0, multiplying up its decays: with P_t the product so far,
 //      h_t = P_t h_in + hz_t, and C_t . h_t = C_t . hz_t + (C_t P_t) . h_in; C_t P_t and the
@@ -33,11 +33,13 @@
 // outside the sequence get Delta = 0 and Delta u = 0, which leave the state as it is.
 //
 // The adjoint, and the states kept for the derivative, are wanted only at segment borders:
-// these modes end with step 3, and are bound by the handovers (about 200 clocks each).
+// these modes end with step 3, and are bound by the handovers (200 to 250 clocks each).  The
+// adjoint, which keeps nothing per token, therefore takes segments of 16 (8 x 4097 tokens x
+// 384 channels: 95 us, 105 with 8).
 //
 // Measured at N = 16, bf16 (the special-function floor in parentheses): 8192 packed tokens x
-// 2048 channels 149 us (74), 4 x 16385 x 384 334 us (111), 8 x 4097 x 384 with kept states
-// 146 us (55); 0.65 instructions a clock and scheduler, shared-memory pipe at 67%.
+// 2048 channels 145 us (74), 4 x 16385 x 384 342 us (111), 8 x 4097 x 384 with kept states
+// 141 us (55), 1 x 16385 x 384 139 us (28); 0.65 instructions a clock and scheduler, shared-memory pipe at 67%.
 #pragma once
 
 #include "causal.cuh"
@@ -68,10 +70,11 @@ enum CausalMode {
 
 namespace {
 
-constexpr int kSeg = 8;             // most tokens of a segment
+constexpr int kSeg = 8;             // tokens of a segment where outputs or kept states are wanted (or half)
+constexpr int kLongSeg = 16;        // and of the adjoint at 16 states, and of calls with few channels
 constexpr int kMostRanked = 64;     // packed sequences that are walked in the order of their lengths
 constexpr int kPassWarps = 8;       // most warps of a CTA: one named barrier each
-static_assert(kCkEvery == kSeg && kAdjEvery % kSeg == 0, "kept states lie at segment borders");
+static_assert(kCkEvery == kSeg && kAdjEvery % kSeg == 0 && kAdjEvery % kLongSeg == 0 && kLongSeg == 2 * kCkEvery, "kept states lie at segment borders");
 
 // sums p[0 .. n) over the n lanes of a channel, which are `stride` apart: the i-th of them
 // gets the sum of p[i].  Each step halves the values a lane holds.
@@ -102,11 +105,12 @@ struct PassWarp {
 __device__ __forceinline__ void named_wait(int id) { asm volatile("barrier.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void named_arrive(int id) { asm volatile("barrier.arrive %0, 64;" ::"r"(id) : "memory"); }
 
-// CTAs of kPassWarps on an SM: the modes without outputs hold fewer registers
-constexpr int pass_ctas(int mode) { return mode == kForward ? 2 : 3; }
+// CTAs of kPassWarps on an SM: the modes without outputs hold fewer registers, outputs of long
+// segments more
+constexpr int pass_ctas(int mode, int seg) { return mode != kForward ? 3 : seg == kLongSeg ? 1 : 2; }
 
 template <typename T, int N, int NL, int SEG, int MODE, bool KEEP, bool VEC>
-__global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(const CausalArgs p) {
+__global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_pass(const CausalArgs p) {
     using S = PassWarp<N, NL, SEG>;
     constexpr int LPC = S::kLanes, CH = S::kCh, NP = NL / 2;
     constexpr int EPL = SEG / LPC;                        // tokens of a segment per lane
@@ -229,8 +233,10 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(
                 const uint32_t word = ok ? rb[k][i * PW / PV] : 0;
                 f[i] = PV == 1 ? bits_f32<T>(word) : word_f32<T>(word, i);
             }
-            if constexpr (PV == 4) {
-                *reinterpret_cast<float4 *>(&sm.bc[k][at]) = make_float4(f[0], f[1], f[2], f[3]);
+            if constexpr (PV % 4 == 0) {
+#pragma unroll
+                for (int i = 0; i < PV; i += 4)
+                    *reinterpret_cast<float4 *>(&sm.bc[k][at + i]) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
             } else if (at < SEG * N) {
 #pragma unroll
                 for (int i = 0; i < PV; ++i) sm.bc[k][at + i] = f[i];
@@ -241,6 +247,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(
 
         // 2. the segment from zero, the product of its decays so far, and what y takes of both
         float2 reach[MODE == kForward ? SEG : 1][NP], part0[MODE == kForward ? SEG : 1], P[NP], hz[NP];
+        float2 midP[NP], midhz[NP];                        // both after the first kCkEvery of a longer segment
 #pragma unroll
         for (int jj = 0; jj < SEG; ++jj) {
             const int j = MODE == kAdjoint ? SEG - 1 - jj : jj;
@@ -264,6 +271,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(
                     part0[j] = i == 0 ? mul2(rowC[i], hz[i]) : fma2(rowC[i], hz[i], part0[j]);
                     reach[j][i] = mul2(rowC[i], P[i]);
                 }
+                if (KEEP && jj == kCkEvery - 1) midP[i] = P[i], midhz[i] = hz[i];
             }
         }
 
@@ -279,9 +287,19 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE)) causal_pass(
         } else if (MODE != kStates && p.state_out && live) {
             store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, out);
         }
-        if (KEEP && MODE != kAdjoint && (SEG == kCkEvery || t0 % kCkEvery == 0) && t0 >= seq.start && live) {
+        if (KEEP && MODE != kAdjoint && (SEG >= kCkEvery || t0 % kCkEvery == 0) && t0 >= seq.start && live) {
             const int64_t row = b * ((p.seqs.L + kCkEvery - 1) / kCkEvery) + t0 / kCkEvery;
             store_row<NP>(p.ckpt + (row * p.d + c) * N + q * NL, h);
+        }
+        if (KEEP && MODE != kAdjoint && SEG > kCkEvery) {  // and the state in the middle
+            const int t = t0 + kCkEvery;
+            if (t >= seq.start && t < seq.end && live) {
+                float2 mid[NP];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) mid[i] = fma2(midP[i], h[i], midhz[i]);
+                const int64_t row = b * ((p.seqs.L + kCkEvery - 1) / kCkEvery) + t / kCkEvery;
+                store_row<NP>(p.ckpt + (row * p.d + c) * N + q * NL, mid);
+            }
         }
         if (MODE == kAdjoint && t0 % kAdjEvery == 0 && t0 > seq.start && live) {
             const int64_t row = b * ((p.seqs.L + kAdjEvery - 1) / kAdjEvery) + t0 / kAdjEvery - 1;
@@ -323,10 +341,17 @@ inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 //     and 92).  Packed, where one sequence may hold most of the tokens, from 16384 on (8192
 //     tokens in 11 sequences x 2048 channels: 147 and 168; in 4: 227 and 164; 4000 tokens in
 //     20 x 768: 45 and 38).
+//   - Where four states a lane give no SM a second CTA, up to 1184 channels, the forward mode
+//     may use all registers, for segments of 16 and half the handovers (2 x 16385 tokens x 384
+//     channels: 176 us against 244; 1 x 4096 x 1184: 49 and 67); and with two states a lane, half
+//     as many instructions again but twice the CTAs, up to 592 (1 x 16385 x 384: 139 us, 244 in
+//     segments of 8; 1 x 4096 x 592: 41 and 67).  Beyond these both lose (4 x 16385 x 384: 342
+//     against 352 and 459).
 //   - Eight warps hide the handover best; four waste less where sequences are short
 //     (64 x 16 tokens x 4096 channels: 68 us against 115; 16 x 200 x 2048: 61 and 68; 64 x
-//     500 x 768: 203 and 209; 11 packed sequences of 745 tokens on average: 162 and 147), and where the CTAs then run in one round instead of a full and a partial one
-//     (8 x 4097 tokens x 384 channels: 141 and 151).  A row has no work for more warps than
+//     500 x 768: 203 and 209; 11 packed sequences of 745 tokens on average: 162 and 147),
+//     and where the CTAs then run in one wave instead of a full and a partial one (8 x 4097
+//     tokens x 384 channels: 141 and 151).  A row has no work for more warps than
 //     segments.
 struct PassPlan {
     int states, seg, warps;
@@ -334,10 +359,12 @@ struct PassPlan {
 inline PassPlan pass_plan(int mode, int N, int64_t channels, bool packed, int64_t tokens_per_seq, int L) {
     PassPlan pl;
     const bool thick = N == 16 && channels >= (packed ? 16384 : 8192);
-    pl.states = thick ? 8 : N >= 8 ? 4 : 2;
-    pl.seg = thick ? 4 : kSeg;
-    const int64_t ctas = channels * N / pl.states / 32, slots = 148 * pass_ctas(mode);
-    pl.warps = tokens_per_seq < 256 || (ctas > slots && ctas <= 2 * slots) ? 4 : kPassWarps;
+    const bool alone = N == 16 && mode == kForward && channels <= 148 * 8;
+    const bool thin = alone && channels <= 148 * 4;
+    pl.states = thick ? 8 : thin || N < 8 ? 2 : 4;
+    pl.seg = thick ? 4 : alone || (mode == kAdjoint && N == 16) ? kLongSeg : kSeg;
+    const int64_t ctas = channels * N / pl.states / 32, slots = 148 * pass_ctas(mode, pl.seg);
+    pl.warps = !alone && (tokens_per_seq < 256 || (ctas > slots && ctas <= 2 * slots)) ? 4 : kPassWarps;
     const int segments = (L + pl.seg - 1) / pl.seg;
     if (segments < pl.warps) pl.warps = segments < 1 ? 1 : segments;
     return pl;
