@@ -257,6 +257,22 @@ def test_time_major_and_far_rows(vs):
     close(y, want, TOL[BF])
 
 
+def test_overlapping_rows(vs):
+    """Rows that are windows over one signal, one element apart."""
+    d, L = 16, 21
+    _, w, b = inputs((1, 1), d, 4, F32, 8)
+    signal = torch.randn(L + d, generator=torch.Generator().manual_seed(8))
+    x = signal.as_strided((2, L, d), (0, 1, 1))
+    dev = signal.cuda().as_strided((2, L, d), (0, 1, 1))
+    y = vs.causal_conv(dev, cuda(w), cuda(b))
+    close(y, causal_ref.conv(x, w, b)[0], TOL[F32])
+    got = vs.causal_conv_bwd(dev, cuda(w), cuda(b), torch.ones_like(y))
+    dense = vs.causal_conv_bwd(dev.contiguous(), cuda(w), cuda(b), torch.ones_like(y))
+    close(got["dx"], dense["dx"].cpu(), TOL[F32])
+    close(got["dw"], dense["dw"].cpu(), SUM_TOL)
+    close(got["db"], dense["db"].cpu(), SUM_TOL)
+
+
 def test_refusals(vs):
     x, w, b = (cuda(t) for t in inputs((2, 10), 32, 4, F32, 1))
     state = torch.zeros((2, 3, 32), device="cuda")

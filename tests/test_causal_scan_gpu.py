@@ -348,6 +348,22 @@ def test_time_major(vs):
     close(y, want, Y_TOL[F32])
 
 
+def test_overlapping_rows(vs):
+    """Activations that are windows over one signal: rows one element apart, shared by the batch."""
+    d, L = 24, 11
+    p = inputs((2, L), d, 16, F32, 9)
+    signal = torch.randn(L + d, generator=torch.Generator().manual_seed(9))
+    p["u"] = signal.as_strided((2, L, d), (0, 1, 1))
+    a = cuda({**p, "u": p["u"].contiguous()})
+    u = a[0] = signal.cuda().as_strided((2, L, d), (0, 1, 1))
+    y = vs.causal_scan(*a)
+    want, _ = ref(p)
+    close(y, want, Y_TOL[F32])
+    got = vs.causal_scan_bwd(*a, torch.ones_like(y))
+    dense = vs.causal_scan_bwd(u.contiguous(), *a[1:], torch.ones_like(y))
+    assert all(torch.equal(got[k], dense[k]) for k in dense)
+
+
 def test_long_sequence(vs):
     """20000 tokens, few channels: many handovers, slow decays."""
     p = inputs((1, 20000), 4, 16, F32, 12)

@@ -859,6 +859,14 @@ def _token_shape(where, x, name, cu_seqlens):
     return (1, *x.shape) if want == 2 else tuple(x.shape)
 
 
+def _new_like(t, zeros=False):
+    """An output laid out like activation ``t``, its channels contiguous even where rows of
+    ``t`` overlap (windows over one signal)."""
+    make = torch.zeros_like if zeros else torch.empty_like
+    y = make(t)
+    return y if y.stride(-1) == 1 else make(t, memory_format=torch.contiguous_format)
+
+
 def causal_ckpt_shape(batch, L, d_inner, d_state):
     """Shape of the states causal_scan(ckpt=...) keeps and causal_scan_bwd(ckpt=...) takes
     (batch 1 and L all tokens with cu_seqlens): [batch, ceil(L / 8), d_inner, d_state]."""
@@ -895,7 +903,7 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
     dt = _dtype_code(u)
     made = None
     if y is None:
-        y = made = torch.empty_like(u)
+        y = made = _new_like(u)
     rows = _i64x[18](
         *_rows(where, "u", u, io, act, dev, packed), *_rows(where, "delta", delta, io, act, dev, packed),
         *_rows(where, "z", z, io, act, dev, packed), *_rows(where, "B", B, io, bc, dev, packed),
@@ -928,7 +936,7 @@ def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=No
     dt = _dtype_code(u)
     made = None
     if y is None:
-        y = made = torch.empty_like(u)
+        y = made = _new_like(u)
     rows = _i64x[18](
         *_rows(where, "u", u, io, act, dev, False), *_rows(where, "delta", delta, io, act, dev, False),
         *_rows(where, "z", z, io, act, dev, False), *_rows(where, "B", B, io, bc, dev, False),
@@ -967,7 +975,7 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
     made = ()
     if out is None:
-        like = torch.zeros_like if packed else torch.empty_like
+        like = lambda t: _new_like(t, packed)
         f = u.new_zeros if packed else u.new_empty
         out = dict(du=like(u), ddelta=like(u), dz=None if z is None else like(u), dB=f(bc, dtype=f32), dC=f(bc, dtype=f32),
                    dA=u.new_empty((Di, N), dtype=f32), dD=u.new_empty(Di, dtype=f32),
@@ -1017,7 +1025,7 @@ def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=No
     io, f32, act = x.dtype, torch.float32, x.shape
     made = None
     if y is None:
-        y = made = torch.empty_like(x)
+        y = made = _new_like(x)
     dt = _dtype_code(x)
     rows = _i64x[6](*_rows(where, "x", x, io, act, dev, packed), *_rows(where, "y", y, io, act, dev, packed))
     pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
@@ -1044,7 +1052,7 @@ def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, slots=None, y
     io, f32, act = x.dtype, torch.float32, x.shape
     made = None
     if y is None:
-        y = made = torch.empty_like(x)
+        y = made = _new_like(x)
     dt = _dtype_code(x)
     rows = _i64x[6](*_rows(where, "x", x, io, act, dev, False), *_rows(where, "y", y, io, act, dev, False))
     pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
@@ -1076,7 +1084,7 @@ def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None
     io, f32, act = x.dtype, torch.float32, x.shape
     made = ()
     if out is None:
-        out = dict(dx=(torch.zeros_like if packed else torch.empty_like)(x), dw=x.new_empty((Ch, W), dtype=f32),
+        out = dict(dx=_new_like(x, packed), dw=x.new_empty((Ch, W), dtype=f32),
                    db=None if b is None else x.new_empty(Ch, dtype=f32))
         made = tuple(out.values())
     elif (b is None) != (out["db"] is None):
