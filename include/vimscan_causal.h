@@ -63,10 +63,11 @@ typedef struct {
  * Causal selective scan:
  *   h_t = exp(Delta_t A) h_(t-1) + Delta_t B_t u_t,  Delta_t = softplus(delta_t + delta_bias)
  *   y_t = (C_t . h_t + D u_t) * silu(z_t)
- *   u, delta, z, y : rows of d_inner channels (dt); z.data may be NULL (no gate).
+ *   u, delta, z, y : rows of d_inner channels (dt); z.data may be NULL (no gate).  y may be
+ *                    u, delta or z itself (the same rows); it must not overlap anything else.
  *   B, C           : rows of d_state (dt), shared by all channels of a token.
  *   A              : [d_inner, d_state] fp32, 16-byte aligned, meant to be <= 0 (of any
- *                    values; with A > 0 the decays of 8 tokens together must stay finite);
+ *                    values; with A > 0 the decays of 16 tokens together must stay finite);
  *                    D, delta_bias : [d_inner] fp32.
  *   seqs           : NULL: batch rows, no states.  States are fp32 [n_slots, d_inner,
  *                    d_state], 16-byte aligned.

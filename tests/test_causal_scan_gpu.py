@@ -364,6 +364,21 @@ def test_overlapping_rows(vs):
     assert all(torch.equal(got[k], dense[k]) for k in dense)
 
 
+@pytest.mark.parametrize("over", [0, 1, 2], ids=["u", "delta", "z"])
+@pytest.mark.parametrize("d", [40, 300, 1300])
+def test_output_over_input(vs, over, d):
+    """y in the place of u, delta or z: the bits of a call with an output of its own."""
+    a = cuda(inputs((2, 75), d, 16, BF, d))
+    y = vs.causal_scan(*a)
+    b = [t.clone() for t in a]
+    assert torch.equal(vs.causal_scan(*b, y=b[over]), y)
+    token = [t[:, 5] if t.dim() == 3 else t for t in a[:5]] + a[5:]
+    state = torch.zeros((2, d, 16), device="cuda")
+    y = vs.causal_scan_step(*token, state.clone())
+    b = [t.clone() for t in token]
+    assert torch.equal(vs.causal_scan_step(*b, state, y=b[over]), y)
+
+
 def test_long_sequence(vs):
     """20000 tokens, few channels: many handovers, slow decays."""
     p = inputs((1, 20000), 4, 16, F32, 12)

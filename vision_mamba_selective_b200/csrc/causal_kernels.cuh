@@ -33,7 +33,7 @@
 // outside the sequence get Delta = 0 and Delta u = 0, which leave the state as it is.
 //
 // The adjoint, and the states kept for the derivative, are wanted only at segment borders:
-// these modes end with step 3, and are bound by the handovers (200 to 250 clocks each).  The
+// these modes end with step 3, and wait mostly for the handovers (200 to 250 clocks each).  The
 // adjoint, which keeps nothing per token, therefore takes segments of 16 (8 x 4097 tokens x
 // 384 channels: 95 us, 105 with 8).
 //
