@@ -10,6 +10,7 @@ kernels; there is no fallback of any kind, and a missing library is an ImportErr
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import struct
 
@@ -1145,16 +1146,17 @@ def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stre
     dev = torch.cuda.current_device()
     try:
         # cheap checks of all at once; what is wrong is worked out only where one fails
+        T = torch.Tensor
         codes = [_CLIP_TYPES.get(t.dtype) for t in src]
-        good = None not in codes and all([t.get_device() == dev and t.is_contiguous() for t in src])
-        at = [t.data_ptr() for t in src]
+        good = None not in codes and set(map(T.get_device, src)) <= {dev} and all(map(T.is_contiguous, src))
+        at = list(map(T.data_ptr, src))
         to = at
         if out is not None:
-            good = good and all([o.get_device() == dev and o.is_contiguous() and o.dtype == t.dtype and o.shape == t.shape
-                                 for t, o in zip(src, dst)])
-            to = [o.data_ptr() for o in dst]
-        table = [v for row in zip(at, to, [t.numel() for t in src], codes) for v in row] if good else None
-    except (AttributeError, RuntimeError):
+            good = good and set(map(T.get_device, dst)) <= {dev} and all(map(T.is_contiguous, dst)) and all(
+                [o.dtype == t.dtype and o.shape == t.shape for t, o in zip(src, dst)])
+            to = list(map(T.data_ptr, dst))
+        table = list(itertools.chain.from_iterable(zip(at, to, map(T.numel, src), codes))) if good else None
+    except (AttributeError, RuntimeError, TypeError):
         table = None
     if table is None:
         for i, (t, o) in enumerate(zip(src, dst)):
