@@ -345,8 +345,9 @@ inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 //     may use all registers, for segments of 16 and half the handovers (2 x 16385 tokens x 384
 //     channels: 176 us against 244; 1 x 4096 x 1184: 49 and 67); and with two states a lane, half
 //     as many instructions again but twice the CTAs, up to 592 (1 x 16385 x 384: 139 us, 244 in
-//     segments of 8; 1 x 4096 x 592: 41 and 67).  Beyond these both lose (4 x 16385 x 384: 342
-//     against 352 and 459).
+//     segments of 8; 1 x 4096 x 592: 41 and 67).  Past 592 the latter loses (4 x 16385 x 384:
+//     459 us against 342), past 1184 the former too (8 x 197 x 192: 14.3 and 12.3; 1 x 4096 x
+//     1600: 98 and 94; only 4 x 16385 x 384 gains, 336 and 342).
 //   - Eight warps hide the handover best; four waste less where sequences are short
 //     (64 x 16 tokens x 4096 channels: 68 us against 115; 16 x 200 x 2048: 61 and 68; 64 x
 //     500 x 768: 203 and 209; 11 packed sequences of 745 tokens on average: 162 and 147),
@@ -356,6 +357,7 @@ inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 struct PassPlan {
     int states, seg, warps;
 };
+// channels: of all sequences together, each sequence's rounded up to a warp's
 inline PassPlan pass_plan(int mode, int N, int64_t channels, bool packed, int64_t tokens_per_seq, int L) {
     PassPlan pl;
     const bool thick = N == 16 && channels >= (packed ? 16384 : 8192);

@@ -23,7 +23,7 @@ vim_status launch_pass_v(const CausalArgs &a, int warps, cudaStream_t stream) {
 template <typename T, int MODE>
 vim_status launch_pass_t(const CausalArgs &a, int N, cudaStream_t stream) {
     const Seqs &q = a.seqs;
-    const PassPlan pl = pass_plan(MODE, N, (int64_t)q.n * a.d, q.cu != nullptr, q.cu ? q.L / q.n : q.L, q.L);
+    const PassPlan pl = pass_plan(MODE, N, (int64_t)q.n * ((a.d + 7) / 8 * 8), q.cu != nullptr, q.cu ? q.L / q.n : q.L, q.L);
     switch (N) {
         case 2: return launch_pass_v<T, 2, 2, 8, MODE>(a, pl.warps, stream);
         case 4: return launch_pass_v<T, 4, 2, 8, MODE>(a, pl.warps, stream);
