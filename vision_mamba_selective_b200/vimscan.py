@@ -223,6 +223,13 @@ def _workspace(nbytes, workspace, device):
         return None, 0
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, nbytes
+    # the kernels write all of it: memory of another device, or elements that share their bytes,
+    # would be written past
+    if not isinstance(workspace, torch.Tensor) or workspace.device != device:
+        raise TypeError(f"workspace must be a tensor on {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     if workspace.numel() * workspace.element_size() < nbytes:
         raise ValueError(f"workspace too small: need {nbytes} bytes")
     return workspace, workspace.numel() * workspace.element_size()
