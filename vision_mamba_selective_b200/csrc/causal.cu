@@ -121,12 +121,9 @@ __global__ void __launch_bounds__(32 * kStepWarps) causal_step(const StepArgs p)
     }
 }
 
-vim_status check_scan(const vim_rows &u, const vim_rows &delta, const vim_rows &z, const vim_rows &B,
-                      const vim_rows &C, const float *A, const float *D, const float *bias, vim_dtype dt) {
-    if (bad_rows(u, dt) || bad_rows(delta, dt) || bad_rows(B, dt) || bad_rows(C, dt) || (z.data && bad_rows(z, dt)))
-        return VIM_ERR_INVALID_ARG;
-    if (!A || !D || !bias || misaligned(A, 16) || misaligned(D, 4) || misaligned(bias, 4)) return VIM_ERR_INVALID_ARG;
-    return VIM_OK;
+bool bad_inputs(const vim_rows &u, const vim_rows &delta, const vim_rows &z, const vim_rows &B, const vim_rows &C,
+                vim_dtype dt) {
+    return bad_rows(u, dt) || bad_rows(delta, dt) || bad_rows(B, dt) || bad_rows(C, dt) || (z.data && bad_rows(z, dt));
 }
 
 }  // namespace
@@ -155,13 +152,9 @@ vim_status causal_scan(const vim_scan_io *io, const float *A, const float *D, co
     if (st != VIM_OK) return st;
     if (ckpt && seqs && seqs->state) return VIM_ERR_INVALID_ARG;   // the derivative starts every sequence from zeros
     if (a.seqs.n == 0 || d_inner == 0) return VIM_OK;
-    if (L > 0) {
-        st = check_scan(u, delta, z, B, C, A, D, delta_bias, dt);
-        if (st != VIM_OK) return st;
-        if (bad_out(y, dt, batch, L, d_inner) || misaligned(ckpt, 16)) return VIM_ERR_INVALID_ARG;
-    } else if (!A || !delta_bias || !D) {
+    if (bad_params(A, D, delta_bias)) return VIM_ERR_INVALID_ARG;   // without tokens too: the kernel loads them first
+    if (L > 0 && (bad_inputs(u, delta, z, B, C, dt) || bad_out(y, dt, batch, L, d_inner) || misaligned(ckpt, 16)))
         return VIM_ERR_INVALID_ARG;
-    }
     a.u = u, a.delta = delta, a.z = z, a.B = B, a.C = C, a.y = y;
     a.A = A, a.D = D, a.bias = delta_bias;
     a.state = static_cast<const float *>(seqs ? seqs->state : nullptr);
@@ -190,9 +183,8 @@ vim_status causal_scan_step(const vim_scan_io *io, const float *A, const float *
     if (st != VIM_OK) return st;
     if (batch == 0 || d_inner == 0) return VIM_OK;
     if (!rows.state) return VIM_ERR_INVALID_ARG;
-    st = check_scan(u, delta, z, B, C, A, D, delta_bias, dt);
-    if (st != VIM_OK) return st;
-    if (bad_out(y, dt, batch, 1, d_inner)) return VIM_ERR_INVALID_ARG;
+    if (bad_params(A, D, delta_bias) || bad_inputs(u, delta, z, B, C, dt) || bad_out(y, dt, batch, 1, d_inner))
+        return VIM_ERR_INVALID_ARG;
     // the kernel's rows are the sequences
     vim_rows in[6] = {u, delta, z, B, C, y};
     for (vim_rows &r : in) {

@@ -30,6 +30,10 @@ inline bool bad_out(const vim_rows &r, vim_dtype dt, int batch, int L, int width
     const bool items_inside = (batch <= 1 || r.batch_stride >= width) && (L <= 1 || r.row_stride >= items);
     return !tokens_inside && !items_inside;
 }
+// the scan's parameters: A is read in vectors of four
+inline bool bad_params(const float *A, const float *D, const float *bias) {
+    return !A || !D || !bias || misaligned(A, 16) || misaligned(D, 4) || misaligned(bias, 4);
+}
 // whether every row of r can be read in vectors of n elements
 inline bool row_vectors(const vim_rows &r, vim_dtype dt, int batch, int L, int n) {
     return !misaligned(r.data, n * elem_size(dt)) && (L <= 1 || r.row_stride % n == 0) &&

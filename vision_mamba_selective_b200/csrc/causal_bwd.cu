@@ -408,8 +408,7 @@ vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const floa
     if (bad_rows(u, dt) || bad_rows(delta, dt) || bad_rows(B, dt) || bad_rows(C, dt) || bad_rows(dout, dt) ||
         (z.data && bad_rows(z, dt)))
         return VIM_ERR_INVALID_ARG;
-    if (!A || !D || !delta_bias || misaligned(A, 16) || misaligned(D, 4) || misaligned(delta_bias, 4))
-        return VIM_ERR_INVALID_ARG;
+    if (bad_params(A, D, delta_bias)) return VIM_ERR_INVALID_ARG;
     if (bad_out(du, dt, batch, L, d_inner) || bad_out(ddelta, dt, batch, L, d_inner)) return VIM_ERR_INVALID_ARG;
     // (an output over an input: other warps may still have to read it)
     for (const vim_rows *o : {&du, &ddelta, &dz})
