@@ -36,7 +36,8 @@ __global__ void __launch_bounds__(32 * kStepWarps) causal_step(const StepArgs p)
     constexpr int WB = NL * (int)sizeof(T) / 4;            // words of a lane's B (C)
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, q = lane % LPC;
     const int blocks = (p.d + CH * kStepWarps - 1) / (CH * kStepWarps);
-    const int c_at = ((int)(blockIdx.x % blocks) * kStepWarps + w) * CH + lane / LPC;
+    const int c_warp = ((int)(blockIdx.x % blocks) * kStepWarps + w) * CH, c_at = c_warp + lane / LPC;
+    if (c_warp >= p.d) return;                             // (it would read what another warp writes in place)
     const int b0 = (int)(blockIdx.x / blocks) * p.per_warp, b1 = min(b0 + p.per_warp, p.seqs.n);
     const bool live = c_at < p.d;
     const int c = live ? c_at : p.d - 1;                   // channels past d repeat the last and write nothing
@@ -46,8 +47,8 @@ __global__ void __launch_bounds__(32 * kStepWarps) causal_step(const StepArgs p)
         const Seq seq = sequence(p.seqs, b0 + lane);
         slot_of = seq.slot < 0 ? -1 : seq.fresh ? -2 - (int)seq.slot : (int)seq.slot;
     }
-    const RowsOf<T> gu(p.u, 0, c), gd(p.delta, 0, c), gz(p.z.data ? p.z : p.u, 0, c), gy(p.y, 0, c);
-    const RowsOf<T> gB(p.B, 0, q * NL), gC(p.C, 0, q * NL);
+    const RowsOf<T, kInPlaceFree> gu(p.u, 0, c), gd(p.delta, 0, c), gz(p.z.data ? p.z : p.u, 0, c);   // y may lie over them
+    const RowsOf<T> gy(p.y, 0, c), gB(p.B, 0, q * NL), gC(p.C, 0, q * NL);
     const float bias = p.bias[c], Dc = p.D[c];
     float A[NL];
 #pragma unroll

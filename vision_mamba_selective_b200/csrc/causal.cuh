@@ -194,9 +194,30 @@ template <typename T> __device__ __forceinline__ float word_f32(uint32_t w, int 
     else return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
 }
 
+// How a kernel loads a tensor: through the non-coherent path, which is for memory that no thread
+// writes while the kernel runs; or by a plain load, where an output may lie over it.  kInPlaceFree
+// (elements and words) is a plain load that stores in between do not hold back: each element is
+// loaded by the thread that writes it, and what it writes depends on the load.  causal_step,
+// 256 x 4096: 31.7 us with it, 32.5 with kInPlace; causal_pass, 4 x 16385 tokens x 384 channels:
+// 339 and 327.
+enum Load { kReadOnly, kInPlace, kInPlaceFree };
+template <Load HOW, typename V> __device__ __forceinline__ V load_as(const char *at) {
+    if constexpr (HOW == kReadOnly) {
+        return __ldg(reinterpret_cast<const V *>(at));
+    } else if constexpr (HOW == kInPlace) {
+        return *reinterpret_cast<const V *>(at);
+    } else {
+        static_assert(sizeof(V) == 4 || sizeof(V) == 2, "elements and words");
+        V v;
+        if constexpr (sizeof(V) == 4) asm("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(at));
+        else asm("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(at));
+        return v;
+    }
+}
+
 // Column `c` of the rows of batch item b.  Row strides fit in 32 bits of bytes (checked on
 // the host), so an address is one widening multiply-add.
-template <typename T>
+template <typename T, Load HOW = kReadOnly>
 struct RowsOf {
     const char *base;
     int row;                                               // bytes between rows
@@ -205,30 +226,30 @@ struct RowsOf {
           row((int)(r.row_stride * (int64_t)sizeof(T))) {}
     __device__ __forceinline__ const char *at(int t) const { return base + (int64_t)t * row; }
     __device__ __forceinline__ uint32_t raw(int t, int i = 0) const {
-        if constexpr (sizeof(T) == 4) return __ldg(reinterpret_cast<const uint32_t *>(at(t)) + i);
-        else return __ldg(reinterpret_cast<const uint16_t *>(at(t)) + i);
+        if constexpr (sizeof(T) == 4) return load_as<HOW, uint32_t>(at(t) + 4 * i);
+        else return load_as<HOW, uint16_t>(at(t) + 2 * i);
     }
     // n 32-bit words of elements: at once, aligned to their size or to four elements, or
     // element by element
     template <int n> __device__ __forceinline__ void words(int t, uint32_t (&v)[n]) const {
         if constexpr (n > (int)sizeof(T)) {                // eight elements
             if constexpr (sizeof(T) == 4) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at(t)));
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at(t)) + 1);
+                const uint4 x = load_as<HOW, uint4>(at(t));
+                const uint4 y = load_as<HOW, uint4>(at(t) + sizeof(uint4));
                 v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
             } else {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at(t)));
-                const uint2 y = __ldg(reinterpret_cast<const uint2 *>(at(t)) + 1);
+                const uint2 x = load_as<HOW, uint2>(at(t));
+                const uint2 y = load_as<HOW, uint2>(at(t) + sizeof(uint2));
                 v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
             }
         } else if constexpr (n == 4) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at(t)));
+            const uint4 x = load_as<HOW, uint4>(at(t));
             v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
         } else if constexpr (n == 2) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at(t)));
+            const uint2 x = load_as<HOW, uint2>(at(t));
             v[0] = x.x, v[1] = x.y;
         } else {
-            v[0] = __ldg(reinterpret_cast<const uint32_t *>(at(t)));
+            v[0] = load_as<HOW, uint32_t>(at(t));
         }
     }
     template <int n> __device__ __forceinline__ void gather(int t, uint32_t (&v)[n]) const {

@@ -153,7 +153,9 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
 
     const vim_rows &urows = MODE == kAdjoint ? p.dout : p.u;
     const bool gate = p.z.data != nullptr;
-    const RowsOf<T> gu(urows, b, c), gd(p.delta, b, c), gz(gate ? p.z : p.u, b, c), gy(p.y, b, c);
+    constexpr Load HOW = MODE == kForward ? kInPlace : kReadOnly;   // y may lie over u, delta or z
+    const RowsOf<T, HOW> gu(urows, b, c), gd(p.delta, b, c), gz(gate ? p.z : p.u, b, c);
+    const RowsOf<T> gy(p.y, b, c);
     const int at = lane * PV;                              // the lane's B (C) values: token, state
     const RowsOf<T> gB(p.B, b, at % N), gC(p.C, b, at % N);
 

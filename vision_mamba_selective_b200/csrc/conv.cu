@@ -43,13 +43,13 @@ struct Strip {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) v[i] = 0;
     }
-    __device__ __forceinline__ void load(const char *at, int left) {
+    template <Load HOW = kReadOnly> __device__ __forceinline__ void load(const char *at, int left) {
         if constexpr (VEC) {
             if constexpr (kWords == 4) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(at));
+                const uint4 q = load_as<HOW, uint4>(at);
                 v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
             } else {
-                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(at));
+                const uint2 q = load_as<HOW, uint2>(at);
                 v[0] = q.x, v[1] = q.y;
             }
         } else {
@@ -57,8 +57,8 @@ struct Strip {
             for (int i = 0; i < V; ++i) {
                 v[i] = 0;
                 if (i < left) {
-                    if constexpr (sizeof(T) == 4) v[i] = __ldg(reinterpret_cast<const uint32_t *>(at) + i);
-                    else v[i] = __ldg(reinterpret_cast<const uint16_t *>(at) + i);
+                    if constexpr (sizeof(T) == 4) v[i] = load_as<HOW, uint32_t>(at + 4 * i);
+                    else v[i] = load_as<HOW, uint16_t>(at + 2 * i);
                 }
             }
         }
@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_prompt(const ConvArgs p)
     }
 }
 
-// One token per sequence: the state row moves up by one.
+// One token per sequence: the state row moves up by one.  A thread reads its channels of the state
+// and of x before it writes any, so both may be written in place.
 template <typename T, int W, int V, bool VEC>
 __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
     const int strips = (p.d + V - 1) / V;
@@ -246,9 +247,9 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
     for (int k = 0; k < W - 1; ++k) {
         x[k].clear();
         if (!q.fresh)
-            x[k].load(reinterpret_cast<const char *>(static_cast<const T *>(p.state) + row + (int64_t)k * p.d), left);
+            x[k].template load<kInPlace>(reinterpret_cast<const char *>(static_cast<const T *>(p.state) + row + (int64_t)k * p.d), left);
     }
-    x[W - 1].load(RowsOf<T>(p.x, b, c).at(0), left);
+    x[W - 1].template load<kInPlace>(RowsOf<T>(p.x, b, c).at(0), left);
     float2 w[W][V / 2], v[V / 2];
     float y[V];
     conv_taps<W, V>(p, c, w, v);
