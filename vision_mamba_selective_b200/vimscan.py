@@ -10,6 +10,7 @@ kernels; there is no fallback of any kind, and a missing library is an ImportErr
 from __future__ import annotations
 
 import ctypes
+import functools
 import itertools
 import os
 import struct
@@ -761,6 +762,29 @@ lib.clip_grad_norm_workspace_bytes.restype = _sz
 # hold nothing but 64-bit values, so they are handed over as packed bytes of those.
 _i64x = {n: struct.Struct(f"{n}q").pack for n in (6, 7, 9, 18, 27)}
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index
+
+
+def _on_stream(entry):
+    """An entry point whose ``stream=`` is the current stream for the whole of the call, so that
+    what it allocates and fills is ordered before its kernels.  Memory of the caller's stream would
+    not do: a fill would run there, and the allocator may take a block that kernels of that stream
+    still use.  The results are recorded on the caller's stream, so that they outlive their use
+    there.  (The inputs are the caller's to order, and to keep until the stream has used them.)"""
+    @functools.wraps(entry)
+    def call(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None:
+            return entry(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            result = entry(*args, **kw)
+        for t in result.values() if isinstance(result, dict) else (result,):
+            if t is not None:
+                t.record_stream(caller)
+        return result
+    return call
+
 
 def _check_ref(where, ref):
     """The device index of the call: that of ``ref``, which must be the current one."""
@@ -844,19 +868,6 @@ def _sequences(where, dev, n_rows, cu_seqlens, state, state_out, slots, fresh, s
     return _i64x[7](pcu or 0, n, pin or 0, pout, pslots or 0, shape[0], pfresh or 0)
 
 
-def _launch_stream(dev, stream, *made):
-    """Raw handle of ``stream`` (default: the current one).  Tensors this call allocated
-    belong to the current stream; used on another, they are recorded there, so that the
-    allocator does not hand their memory out while the kernels still use it."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
-    return stream.cuda_stream
-
-
 def _token_shape(where, x, name, cu_seqlens):
     """(batch, L, channels) of the activations [batch, L, c], or [L, c] with cu_seqlens."""
     want = 3 if cu_seqlens is None else 2
@@ -881,6 +892,7 @@ def causal_ckpt_shape(batch, L, d_inner, d_state):
     return (batch, (L + 7) // 8, d_inner, d_state)
 
 
+@_on_stream
 def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=None, state_out=None, slots=None,
                 fresh=None, ckpt=None, y=None, stream=None):
     """Causal selective scan; see include/vimscan_causal.h.
@@ -909,9 +921,8 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
     packed = cu_seqlens is not None
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
     dt = _dtype_code(u)
-    made = None
     if y is None:
-        y = made = _new_like(u)
+        y = _new_like(u)
     rows = _i64x[18](
         *_rows(where, "u", u, io, act, dev, packed), *_rows(where, "delta", delta, io, act, dev, packed),
         *_rows(where, "z", z, io, act, dev, packed), *_rows(where, "B", B, io, bc, dev, packed),
@@ -920,12 +931,13 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
     pbias = _table(where, "delta_bias", delta_bias, f32, (Di,), dev)
     pk = None if ckpt is None else _table(where, "ckpt", ckpt, f32, causal_ckpt_shape(batch, L, Di, N), dev)
     seqs = _sequences(where, dev, batch, cu_seqlens, state, state_out, slots, fresh, f32, (Di, N))
-    st = lib.causal_scan(rows, pA, pD, pbias, batch, L, Di, N, dt, seqs, pk, _launch_stream(dev, stream, made))
+    st = lib.causal_scan(rows, pA, pD, pbias, batch, L, Di, N, dt, seqs, pk, _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
 
 
+@_on_stream
 def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=None, slots=None, y=None, stream=None):
     """causal_scan for one token of each sequence: u, delta, z [batch, d_inner], B, C
     [batch, d_state], state as there (required; updated in place unless ``state_out`` is
@@ -942,9 +954,8 @@ def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=No
     N = B.shape[-1]
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (batch, N)
     dt = _dtype_code(u)
-    made = None
     if y is None:
-        y = made = _new_like(u)
+        y = _new_like(u)
     rows = _i64x[18](
         *_rows(where, "u", u, io, act, dev, False), *_rows(where, "delta", delta, io, act, dev, False),
         *_rows(where, "z", z, io, act, dev, False), *_rows(where, "B", B, io, bc, dev, False),
@@ -952,7 +963,7 @@ def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=No
     pA, pD = _table(where, "A", A, f32, (Di, N), dev), _table(where, "D", D, f32, (Di,), dev)
     pbias = _table(where, "delta_bias", delta_bias, f32, (Di,), dev)
     seqs = _sequences(where, dev, batch, None, state, state_out, slots, None, f32, (Di, N))
-    st = lib.causal_scan_step(rows, pA, pD, pbias, batch, Di, N, dt, seqs, _launch_stream(dev, stream, made))
+    st = lib.causal_scan_step(rows, pA, pD, pbias, batch, Di, N, dt, seqs, _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
@@ -962,6 +973,7 @@ def causal_bwd_workspace_bytes(batch, L, d_inner, d_state, has_ckpt):
     return int(lib.causal_bwd_workspace_bytes(batch, L, d_inner, d_state, int(bool(has_ckpt))))
 
 
+@_on_stream
 def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=None, ckpt=None, workspace=None, out=None,
                     stream=None):
     """Derivatives of causal_scan, for sequences that start from zeros and whose final states
@@ -981,14 +993,12 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     N = B.shape[-1]
     packed = cu_seqlens is not None
     io, f32, act, bc = u.dtype, torch.float32, u.shape, (*u.shape[:-1], N)
-    made = ()
     if out is None:
         like = lambda t: _new_like(t, packed)
         f = u.new_zeros if packed else u.new_empty
         out = dict(du=like(u), ddelta=like(u), dz=None if z is None else like(u), dB=f(bc, dtype=f32), dC=f(bc, dtype=f32),
                    dA=u.new_empty((Di, N), dtype=f32), dD=u.new_empty(Di, dtype=f32),
                    ddelta_bias=u.new_empty(Di, dtype=f32))
-        made = tuple(out.values())
     elif (z is None) != (out["dz"] is None):
         raise ValueError(f"{where}: out['dz'] must be given exactly when z is")
     dt = _dtype_code(u)
@@ -1004,17 +1014,17 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     rows = _i64x[27](
         *r("u", u, act), *r("delta", delta, act), *r("z", z, act), *r("B", B, bc), *r("C", C, bc), *r("dout", dout, act),
         *r("out['du']", out["du"], act), *r("out['ddelta']", out["ddelta"], act), *r("out['dz']", out["dz"], act))
-    given = workspace
     ws, ws_bytes = _workspace(causal_bwd_workspace_bytes(batch, L, Di, N, ckpt is not None), workspace, u.device)
     st = lib.causal_scan_bwd(
         rows, pA, pD, pbias, pdB, pdC, pdA, pdD, pdb, batch, L, Di, N, dt, pcu, n, pk,
         None if ws is None else ws.data_ptr(), ws_bytes,
-        _launch_stream(dev, stream, *made, *(() if given is not None else (ws,))))
+        _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return out
 
 
+@_on_stream
 def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=None, slots=None, fresh=None, y=None,
                 stream=None):
     """Short causal depthwise convolution, with SiLU unless ``silu`` is false; see
@@ -1031,19 +1041,19 @@ def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=No
     W = w.shape[-1]
     packed = cu_seqlens is not None
     io, f32, act = x.dtype, torch.float32, x.shape
-    made = None
     if y is None:
-        y = made = _new_like(x)
+        y = _new_like(x)
     dt = _dtype_code(x)
     rows = _i64x[6](*_rows(where, "x", x, io, act, dev, packed), *_rows(where, "y", y, io, act, dev, packed))
     pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
     seqs = _sequences(where, dev, batch, cu_seqlens, state, state_out, slots, fresh, io, (W - 1, Ch))
-    st = lib.causal_conv(rows, pw, pb, batch, L, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(dev, stream, made))
+    st = lib.causal_conv(rows, pw, pb, batch, L, Ch, W, int(bool(silu)), dt, seqs, _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
 
 
+@_on_stream
 def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, slots=None, y=None, stream=None):
     """causal_conv for one token of each sequence: x [batch, channels]; state as there
     (required; updated in place unless ``state_out`` is given).  Rows whose slot is outside
@@ -1058,14 +1068,13 @@ def causal_conv_step(x, w, b, state, *, silu=True, state_out=None, slots=None, y
     batch, Ch = x.shape
     W = w.shape[-1]
     io, f32, act = x.dtype, torch.float32, x.shape
-    made = None
     if y is None:
-        y = made = _new_like(x)
+        y = _new_like(x)
     dt = _dtype_code(x)
     rows = _i64x[6](*_rows(where, "x", x, io, act, dev, False), *_rows(where, "y", y, io, act, dev, False))
     pw, pb = _table(where, "w", w, f32, (Ch, W), dev), _table(where, "b", b, f32, (Ch,), dev)
     seqs = _sequences(where, dev, batch, None, state, state_out, slots, None, io, (W - 1, Ch))
-    st = lib.causal_conv_step(rows, pw, pb, batch, Ch, W, int(bool(silu)), dt, seqs, _launch_stream(dev, stream, made))
+    st = lib.causal_conv_step(rows, pw, pb, batch, Ch, W, int(bool(silu)), dt, seqs, _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return y
@@ -1075,6 +1084,7 @@ def causal_conv_bwd_workspace_bytes(batch, L, channels, width):
     return int(lib.causal_conv_bwd_workspace_bytes(batch, L, channels, width))
 
 
+@_on_stream
 def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None, out=None, stream=None):
     """Derivatives of causal_conv, for sequences that start from zeros and whose final states
     are not used, and a loss whose derivative with respect to y is ``dout``; see
@@ -1090,11 +1100,9 @@ def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None
     W = w.shape[-1]
     packed = cu_seqlens is not None
     io, f32, act = x.dtype, torch.float32, x.shape
-    made = ()
     if out is None:
         out = dict(dx=_new_like(x, packed), dw=x.new_empty((Ch, W), dtype=f32),
                    db=None if b is None else x.new_empty(Ch, dtype=f32))
-        made = tuple(out.values())
     elif (b is None) != (out["db"] is None):
         raise ValueError(f"{where}: out['db'] must be given exactly when b is")
     dt = _dtype_code(x)
@@ -1104,11 +1112,10 @@ def causal_conv_bwd(x, w, b, dout, *, silu=True, cu_seqlens=None, workspace=None
     pdw, pdb = tab("out['dw']", out["dw"], (Ch, W)), tab("out['db']", out["db"], (Ch,))
     r = lambda name, t: _rows(where, name, t, io, act, dev, packed)
     rows = _i64x[9](*r("x", x), *r("dout", dout), *r("out['dx']", out["dx"]))
-    given = workspace
     ws, ws_bytes = _workspace(causal_conv_bwd_workspace_bytes(batch, L, Ch, W), workspace, x.device)
     st = lib.causal_conv_bwd(rows, pw, pb, pdw, pdb, batch, L, Ch, W, int(bool(silu)), dt, pcu, n,
                              None if ws is None else ws.data_ptr(), ws_bytes,
-                             _launch_stream(dev, stream, *made, *(() if given is not None else (ws,))))
+                             _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return out
@@ -1132,6 +1139,7 @@ def _refuse_gradient(where, name, t, dev):
         raise TypeError(f"{where}: {name}: unsupported dtype {t.dtype}: fp32 or bf16")
 
 
+@_on_stream
 def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
     """The common norm of many gradients, and clipping by it; see include/vimscan_causal.h.
 
@@ -1174,19 +1182,14 @@ def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stre
                                  f"{tuple(o.shape)}")
         raise TypeError(f"{where}: grads and out must be tensors with storage")
     device = torch.device("cuda", dev)
-    made = []
     if norm is None:
         norm = src[0].new_empty(1, dtype=torch.float32) if src else torch.empty(1, dtype=torch.float32, device=device)
-        made.append(norm)
     elif not isinstance(norm, torch.Tensor) or norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
         raise ValueError(f"{where}: norm must be one float32 element on cuda:{dev}")
     n = len(src)
-    given = workspace
     ws, ws_bytes = _workspace(clip_grad_norm_workspace_bytes(n), workspace, device)
-    if given is None:
-        made.append(ws)
     st = lib.clip_grad_norm(struct.pack(f"{4 * n}q", *table), n, max_norm, norm.data_ptr(), ws.data_ptr(), ws_bytes,
-                            _launch_stream(dev, stream, *made))
+                            _raw_stream(dev))
     if st != VIM_OK:
         raise VimScanError(st, where)
     return norm
