@@ -219,6 +219,27 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on_stream(entry):
+    """An entry point whose ``stream=`` is the current stream for the whole of the call, so that
+    what it allocates and fills is ordered before its kernels.  Memory of the caller's stream would
+    not do: a fill would run there, and the allocator may take a block that kernels of that stream
+    still use.  The results are recorded on the caller's stream, so that they outlive their use
+    there.  (The inputs are the caller's to order, and to keep until the stream has used them.)"""
+    @functools.wraps(entry)
+    def call(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None:
+            return entry(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            result = entry(*args, **kw)
+        for t in result.values() if isinstance(result, dict) else (result,):
+            if t is not None and t.is_cuda:
+                t.record_stream(caller)
+        return result
+    return call
+
+
 def _workspace(nbytes, workspace, device):
     if nbytes == 0:
         return None, 0
@@ -297,6 +318,7 @@ def ckpt_shape(batch, L, d_inner, d_state):
     return (batch, (L + 31) // 32, 2, d_state, d_inner)
 
 
+@_on_stream
 def vim_scan_bidir(u, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_stride=0,
                    workspace=None, stream=None, events=None, zoh=False, ckpt=None):
     """Vim bidirectional selective scan, (y^f + y^b) * silu(z); see include/vimscan.h.
@@ -312,6 +334,7 @@ def vim_scan_bidir(u, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_stride
                   workspace, stream, events, zoh, ckpt)
 
 
+@_on_stream
 def vim_scan_bidir_conv(x, conv_w, conv_b, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_stride=0,
                         workspace=None, stream=None, events=None, zoh=False, ckpt=None):
     """vim_scan_bidir with the pathways' kernel-3 convolution + SiLU front fused in.
@@ -329,6 +352,7 @@ def vim_scan_bwd_workspace_bytes(batch, L, d_inner, d_state, separate_bc):
     return int(lib.vim_scan_bwd_workspace_bytes(batch, L, d_inner, d_state, int(bool(separate_bc))))
 
 
+@_on_stream
 def vim_scan_bidir_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, bc_dir_stride=0, workspace=None,
                        stream=None, out=None, events=None, zoh=False, ckpt=None):
     """Derivatives of vim_scan_bidir (first-order Bbar, or with ``zoh`` the exact
@@ -393,6 +417,7 @@ def vim_scan_conv_bwd_workspace_bytes(batch, L, d_inner, d_state, dtype_code, se
     return int(lib.vim_scan_conv_bwd_workspace_bytes(batch, L, d_inner, d_state, dtype_code, int(bool(separate_bc))))
 
 
+@_on_stream
 def vim_scan_bidir_conv_bwd(x, conv_w, conv_b, delta, z, B, C, A, D, delta_bias, dout, *, bc_dir_stride=0,
                             workspace=None, stream=None, out=None, zoh=False, ckpt=None):
     """Derivatives of vim_scan_bidir_conv (first-order Bbar, or with ``zoh`` the exact
@@ -450,6 +475,7 @@ def vim_scan_bidir_conv_bwd(x, conv_w, conv_b, delta, z, B, C, A, D, delta_bias,
     return out
 
 
+@_on_stream
 def vmamba_cross_scan4_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, workspace=None, stream=None, out=None,
                            zoh=False, ckpt=None):
     """Derivatives of vmamba_cross_scan4 (first-order Bbar, or with ``zoh`` the exact
@@ -499,6 +525,7 @@ def vim_block_workspace_bytes(batch, L, d_inner, d_state):
     return int(lib.vim_block_workspace_bytes(batch, L, d_inner, d_state))
 
 
+@_on_stream
 def vim_block_scan(x, Wx, Wdt, dt_bias, A, D, z, *, conv_w=None, conv_b=None, y=None, workspace=None,
                    stream=None, events=None):
     """The Vim block's two S6 modules from their common input x with their own
@@ -530,6 +557,7 @@ def vim_block_bwd_workspace_bytes(batch, L, d_inner, d_state):
     return int(lib.vim_block_bwd_workspace_bytes(batch, L, d_inner, d_state))
 
 
+@_on_stream
 def vim_block_scan_bwd(x, Wx, Wdt, dt_bias, A, D, z, dout, *, conv_w=None, conv_b=None, workspace=None, stream=None,
                        out=None):
     """Derivatives of vim_block_scan for a loss whose derivative with respect to y is
@@ -573,6 +601,7 @@ def vim_block_scan_bwd(x, Wx, Wdt, dt_bias, A, D, z, dout, *, conv_w=None, conv_
     return out
 
 
+@_on_stream
 def vim_scan_bidir_noalloc(u, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_stride=0, stream=None):
     """vim_scan_bidir without a workspace, for callers that cannot allocate device memory.
 
@@ -607,6 +636,7 @@ def cross_ckpt_shape(batch, H, W, channels, d_state):
     return (2,) + ckpt_shape(batch, H * W, channels, d_state)
 
 
+@_on_stream
 def vmamba_cross_scan4(u, delta, z, B, C, A, D, delta_bias, *, y=None, workspace=None, stream=None,
                        events=None, zoh=False, ckpt=None):
     """VMamba four-direction cross-scan with CS-Merge; see include/vimscan.h.
@@ -646,6 +676,7 @@ def vmamba_cross_scan4(u, delta, z, B, C, A, D, delta_bias, *, y=None, workspace
     return y
 
 
+@_on_stream
 def cross_merge4(ys, z, H, W, *, y=None, stream=None):
     """CS-Merge alone: ys [4, batch, H*W, C] in scan order -> y [batch, H, W, C]."""
     _, batch, L, Ch = ys.shape
@@ -678,6 +709,7 @@ def _host_streams(device):
     return _copy_streams[idx]
 
 
+@_on_stream
 def vim_scan_bidir_host(u, delta, z, B, C, A, D, delta_bias, *, y=None, bc_dir_stride=0, slices=4,
                         workspace=None, stream=None, upload=None, download=None, zoh=False):
     """vim_scan_bidir for activations in host memory; see include/vimscan.h.
@@ -763,27 +795,6 @@ lib.clip_grad_norm_workspace_bytes.restype = _sz
 _i64x = {n: struct.Struct(f"{n}q").pack for n in (6, 7, 9, 18, 27)}
 
 _raw_stream = torch._C._cuda_getCurrentRawStream   # of a device index
-
-
-def _on_stream(entry):
-    """An entry point whose ``stream=`` is the current stream for the whole of the call, so that
-    what it allocates and fills is ordered before its kernels.  Memory of the caller's stream would
-    not do: a fill would run there, and the allocator may take a block that kernels of that stream
-    still use.  The results are recorded on the caller's stream, so that they outlive their use
-    there.  (The inputs are the caller's to order, and to keep until the stream has used them.)"""
-    @functools.wraps(entry)
-    def call(*args, **kw):
-        stream = kw.get("stream")
-        if stream is None:
-            return entry(*args, **kw)
-        caller = torch.cuda.current_stream(stream.device)
-        with torch.cuda.stream(stream):
-            result = entry(*args, **kw)
-        for t in result.values() if isinstance(result, dict) else (result,):
-            if t is not None:
-                t.record_stream(caller)
-        return result
-    return call
 
 
 def _check_ref(where, ref):
