@@ -34,3 +34,23 @@ def test_parameters_of_an_empty_prompt(vs):
     for A, D, bias in ((FAKE + 4, FAKE, FAKE), (FAKE, FAKE + 2, FAKE), (FAKE, FAKE, FAKE + 2), (None, FAKE, FAKE),
                        (FAKE, None, FAKE), (FAKE, FAKE, None)):
         assert scan(vs, none, A, D, bias, L=0, seqs=seqs) == vs.VIM_ERR_INVALID_ARG, (A, D, bias)
+
+
+def test_gradients_and_their_outputs_are_paired(vs):
+    """Dicts by key, whatever their order; lists and tuples by place; None where the other is."""
+    a, b, c, d = (torch.zeros(2) for _ in range(4))
+    pairs = lambda grads, out: vs._clip_pairs("clip_grad_norm", grads, out)
+    same = lambda got, want: all(len(x) == len(y) and all(p is q for p, q in zip(x, y)) for x, y in zip(got, want))
+    assert same(pairs(dict(dD=a, dz=None, dA=b), dict(dA=d, dz=None, dD=c)), ([a, b], [c, d]))
+    assert same(pairs([a, None, b], (c, None, d)), ([a, b], [c, d]))
+    assert same(pairs(dict(dD=a, dz=None), None), ([a], [a]))
+    assert same(pairs((t for t in (a, b)), None), ([a, b], [a, b]))
+    assert same(pairs((t for t in (a, b)), iter([c, d])), ([a, b], [c, d]))
+    assert same(pairs([], []), ([], []))
+    for grads, out in ((dict(dD=a), dict(dA=c)), (dict(dD=a, dA=b), dict(dD=c)), (dict(dD=a), dict(dD=c, dA=None)),
+                       (dict(dD=a, dA=None), dict(dD=None, dA=c)), ([None, a], [c, None]), ([a], [c, None]), ([a, b], [c])):
+        with pytest.raises(ValueError):
+            pairs(grads, out)
+    for grads, out in ((dict(dD=a), [c]), ([a], dict(dD=c))):
+        with pytest.raises(TypeError):
+            pairs(grads, out)

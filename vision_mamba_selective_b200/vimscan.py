@@ -1150,22 +1150,41 @@ def _refuse_gradient(where, name, t, dev):
         raise TypeError(f"{where}: {name}: unsupported dtype {t.dtype}: fp32 or bf16")
 
 
+def _clip_pairs(where, grads, out):
+    """The gradients and the output of each, as two lists: dicts are paired by key, lists and tuples
+    by place; entries that are None on both sides are skipped."""
+    if out is None:
+        src = [t for t in (grads.values() if isinstance(grads, dict) else grads) if t is not None]
+        return src, src
+    if isinstance(grads, dict) != isinstance(out, dict):
+        raise TypeError(f"{where}: grads and out must both be dicts, or both lists or tuples")
+    if isinstance(grads, dict):
+        if grads.keys() != out.keys():
+            raise ValueError(f"{where}: grads has the keys {list(grads)}, out {list(out)}")
+        grads, out = grads.values(), [out[k] for k in grads]
+    else:
+        grads, out = list(grads), list(out)
+    src, dst = [t for t in grads if t is not None], [o for o in out if o is not None]
+    if len(grads) != len(out) or len(src) != len(dst):
+        raise ValueError(f"{where}: {len(src)} gradients and {len(dst)} outputs")
+    if len(src) != len(grads) and [t is None for t in grads] != [o is None for o in out]:
+        raise ValueError(f"{where}: an output must be None exactly where its gradient is")
+    return src, dst
+
+
 @_on_stream
 def clip_grad_norm(grads, max_norm, *, out=None, norm=None, workspace=None, stream=None):
     """The common norm of many gradients, and clipping by it; see include/vimscan_causal.h.
 
     ``grads``: contiguous CUDA tensors, fp32 or bf16 in any mixture, as a list or tuple, or a
     dict of them as the *_bwd functions return (None entries are skipped).  They are scaled
-    in place by min(1, max_norm / (norm + 1e-6)), or into ``out`` (the same kind of
-    collection, the same shapes and dtypes).  A norm that is not finite scales nothing.
+    in place by min(1, max_norm / (norm + 1e-6)), or into ``out`` (a dict with the same keys, or
+    a list or tuple in the same order; the same shapes and dtypes, None where grads has it).  A norm that is not finite scales nothing.
     max_norm may be infinite: then nothing but the norm is computed.  Returns the norm, a
     float32 tensor of one element on the device (``norm`` if given).
     """
     where = "clip_grad_norm"
-    src = [t for t in (grads.values() if isinstance(grads, dict) else grads) if t is not None]
-    dst = src if out is None else [t for t in (out.values() if isinstance(out, dict) else out) if t is not None]
-    if len(dst) != len(src):
-        raise ValueError(f"{where}: {len(src)} gradients and {len(dst)} outputs")
+    src, dst = _clip_pairs(where, grads, out)
     max_norm = float(max_norm)
     if not max_norm >= 0:
         raise ValueError(f"{where}: max_norm must be >= 0, got {max_norm}")
