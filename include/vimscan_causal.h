@@ -73,8 +73,8 @@ typedef struct {
  *                    d_state], 16-byte aligned.
  *   ckpt           : NULL, or fp32 causal_ckpt_bytes(batch, L, d_inner, d_state) bytes,
  *                    16-byte aligned: the state entering every 8th token of a row,
- *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd.  Not
- *                    together with initial states (VIM_ERR_INVALID_ARG): the derivative
+ *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd; those
+ *                    of padding entries too.  Not together with initial states (VIM_ERR_INVALID_ARG): the derivative
  *                    starts every sequence from zeros.
  * One launch, no workspace.
  */
@@ -104,7 +104,10 @@ vim_status causal_scan_step(const vim_scan_io *io, const float *A, const float *
  *   dB, dC    : fp32 [batch, L, d_state], contiguous, written.
  *   dA [d_inner, d_state], dD [d_inner], ddelta_bias [d_inner] : fp32, written.
  *   cu_seqlens, n_seqs : as in vim_sequences (NULL: one sequence per batch row).  Rows of
- *               no sequence keep what they held in every output.
+ *               no sequence keep what they held in every output.  There are no slots here:
+ *               a sequence that causal_scan skipped as a padding entry is differentiated
+ *               like any other, so its dout is to be zero and its inputs finite (or the
+ *               offsets are to leave it out).
  *   ckpt      : what causal_scan kept for the same inputs, or NULL: formed here.
  *   workspace : causal_bwd_workspace_bytes(batch, L, d_inner, d_state, ckpt != NULL) bytes,
  *               256-byte aligned.

@@ -27,3 +27,36 @@ def test_clipping_into_a_dict_in_another_order(vs):
         vs.clip_grad_norm(grads, 0.5, out={**out, "dz": out["db"]})
     with pytest.raises(TypeError):
         vs.clip_grad_norm(grads, 0.5, out=[t for t in out.values() if t is not None])
+
+
+@pytest.mark.parametrize("d,N,dtype", [(40, 16, F32), (300, 16, BF), (1300, 16, F32), (6000, 16, BF), (24, 8, F32), (20, 2, F32)])
+def test_kept_states_of_padding_entries(vs, d, N, dtype):
+    """A padding slot skips the outputs and the final state of a sequence, not the states that are
+    kept for the derivative: it takes every sequence that cu_seqlens lists and knows no slots."""
+    lens = [21, 50, 0, 9, 33]
+    p, cu = packed_case(lens, d, N, dtype, seed=d, lead=2, tail=3)
+    args = cuda(p)
+    dev = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    shape = vs.causal_ckpt_shape(1, cu[-1] + 3, d, N)
+    plain, some, all_skipped = (torch.full(shape, float("nan"), device="cuda") for _ in range(3))
+    state = torch.full((5, d, N), 7.0, device="cuda")
+    y0 = torch.full_like(args[0], 3.0)
+    vs.causal_scan(*args, ckpt=plain, state_out=state, y=y0, **dev)
+    for slots, ck in (([4, -1, 0, 9, 2], some), ([5, -1, 7, 9, -3], all_skipped)):
+        y, out = torch.full_like(args[0], 3.0), torch.full((5, d, N), 7.0, device="cuda")
+        vs.causal_scan(*args, ckpt=ck, state_out=out, y=y, slots=torch.tensor(slots, dtype=torch.int32, device="cuda"), **dev)
+        torch.cuda.synchronize()
+        kept = ~torch.isnan(plain)
+        assert torch.equal(torch.isnan(ck), torch.isnan(plain)) and torch.equal(ck[kept], plain[kept])
+        used = {s for s in slots if 0 <= s < 5}
+        for s, (slot, t0, t1) in enumerate(zip(slots, cu[:-1], cu[1:])):
+            if slot in used:
+                assert torch.equal(y[t0:t1], y0[t0:t1]) and torch.equal(out[slot], state[s])
+            else:
+                assert (y[t0:t1] == 3.0).all()
+        assert all((out[i] == 7.0).all() for i in range(5) if i not in used)
+    dout = torch.randn(args[0].shape, generator=torch.Generator().manual_seed(d)).to(dtype).cuda()
+    want = vs.causal_scan_bwd(*args, dout, ckpt=plain, **dev)
+    got = vs.causal_scan_bwd(*args, dout, ckpt=some, **dev)
+    for k in want:
+        assert torch.equal(got[k], want[k]), k

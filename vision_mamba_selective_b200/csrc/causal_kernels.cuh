@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
     const int q = lane / CH, cl = lane % CH;
     const bool live = c0 + cl < p.d;
     const int c = live ? c0 + cl : p.d - 1;                // lanes past d repeat the last channel and write nothing
-    if (seq.slot < 0) return;                              // a padding entry
+    if (seq.slot < 0 && !KEEP) return;                     // a padding entry
+    const bool put = live && (!KEEP || seq.slot >= 0);     // (its kept states are wanted all the same)
 
     const vim_rows &urows = MODE == kAdjoint ? p.dout : p.u;
     const bool gate = p.z.data != nullptr;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
         for (int i = 0; i < NP; ++i) h0[i] = f2(0.0f, 0.0f);
         if (p.state && !seq.fresh) load_row<NP>(p.state + (seq.slot * p.d + c) * N + q * NL, h0);
         store_row<NP>(&sm.carry[lane * NL], h0);
-        if (M == 0 && MODE != kStates && p.state_out && live)
+        if (M == 0 && MODE != kStates && p.state_out && put)
             store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, h0);
     }
     if (w < M) fetch(w);
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
         if (m + 1 < M) {
             store_row<NP>(&next.carry[lane * NL], out);
             if (W > 1) named_arrive(w + 1 == W ? 0 : w + 1);
-        } else if (MODE != kStates && p.state_out && live) {
+        } else if (MODE != kStates && p.state_out && put) {
             store_row<NP>(p.state_out + (seq.slot * p.d + c) * N + q * NL, out);
         }
         if (KEEP && MODE != kAdjoint && (SEG >= kCkEvery || t0 % kCkEvery == 0) && t0 >= seq.start && live) {
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
                 }
                 const float y = fmaf(Dc, u_own[e], reduce_scatter<LPC, CH>(part, q)) * z_own[e];
                 const int t = t0 + e * LPC + q;
-                if (live && (unsigned)(t - seq.start) < length) gy.put(t, y);
+                if (put && (unsigned)(t - seq.start) < length) gy.put(t, y);
             }
         }
         __syncwarp();                                      // the warp's shared memory may be written again

@@ -996,7 +996,8 @@ def causal_scan_bwd(u, delta, z, B, C, A, D, delta_bias, dout, *, cu_seqlens=Non
     ddelta_bias [d_inner] (fp32).  ``out`` may hold those tensors from an earlier call to be
     written again (du, ddelta and dz with any row strides).  Tokens of no sequence keep what
     the outputs held (zeros when allocated here).  ``ckpt``: the states causal_scan(ckpt=...)
-    kept for the same inputs.
+    kept for the same inputs.  Every sequence counts, those that a padding slot made
+    causal_scan skip as well: give them a dout of zero and finite inputs.
     """
     where = "causal_scan_bwd"
     dev = _check_ref(where, u)
