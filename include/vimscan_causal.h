@@ -74,8 +74,9 @@ typedef struct {
  *   ckpt           : NULL, or fp32 causal_ckpt_bytes(batch, L, d_inner, d_state) bytes,
  *                    16-byte aligned: the state entering every 8th token of a row,
  *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd; those
- *                    of padding entries too.  Not together with initial states (VIM_ERR_INVALID_ARG): the derivative
- *                    starts every sequence from zeros.
+ *                    of padding entries too.  Not together with initial states
+ *                    (VIM_ERR_INVALID_ARG): the derivative starts every sequence from
+ *                    zeros.
  * One launch, no workspace.
  */
 typedef struct {
@@ -179,7 +180,7 @@ typedef struct {
  *               contiguous, empty ones allowed.  An `out` must not overlap any other tensor.
  *   max_norm  : >= 0; infinity clips nothing and, in place, writes nothing but the norm.
  *   workspace : clip_grad_norm_workspace_bytes(count) bytes, 256-byte aligned.
- * A norm that is NaN or infinite clips nothing: `out` gets the gradients as they are, and the
+ * A norm that is NaN or infinite (in fp32) clips nothing: `out` gets the gradients as they are, and the
  * caller sees the norm.  The sum is formed in fp64 in a fixed order.  Two launches for every
  * 120 tensors.
  */

@@ -60,3 +60,16 @@ def test_kept_states_of_padding_entries(vs, d, N, dtype):
     got = vs.causal_scan_bwd(*args, dout, ckpt=some, **dev)
     for k in want:
         assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_norm_past_fp32_scales_nothing(vs, dtype):
+    """A norm that is infinite in fp32, although every gradient and the sum in fp64 are finite, is
+    what the caller sees, and leaves the gradients as they are."""
+    src = [torch.full((40,), 2e38, device="cuda").to(dtype), torch.ones(7, device="cuda")]
+    before = [t.clone() for t in src]
+    out = [torch.zeros_like(t) for t in src]
+    assert vs.clip_grad_norm(src, 1.0, out=out).item() == math.inf
+    assert all(torch.equal(a, b) for a, b in zip(out, before))
+    assert vs.clip_grad_norm(src, 1.0).item() == math.inf
+    assert all(torch.equal(a, b) for a, b in zip(src, before))

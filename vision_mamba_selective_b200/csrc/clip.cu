@@ -130,10 +130,11 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale(const __grid_constant
     double s = 0.0;
     for (int i = threadIdx.x; i < parts; i += kClipThreads) s += part[i];
     const double total = sqrt(cta_sum(s, sums));
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
-    // a norm that is not finite clips nothing: the gradients stay as they are
+    const float seen = (float)total;                       // the norm that the caller sees
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = seen;
+    // one that is not finite clips nothing: the gradients stay as they are
     const double ratio = (double)max_norm / (total + 1.0e-6);
-    const float factor = total < INFINITY && ratio < 1.0 ? (float)ratio : 1.0f;
+    const float factor = seen < INFINITY && ratio < 1.0 ? (float)ratio : 1.0f;
     if (factor == 1.0f && in_place) return;
     for (int u = t.units - 1 - blockIdx.x; u >= 0; u -= gridDim.x) {
         const int k = clip_tensor(t, u);
