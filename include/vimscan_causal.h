@@ -180,9 +180,9 @@ typedef struct {
  *               contiguous, empty ones allowed.  An `out` must not overlap any other tensor.
  *   max_norm  : >= 0; infinity clips nothing and, in place, writes nothing but the norm.
  *   workspace : clip_grad_norm_workspace_bytes(count) bytes, 256-byte aligned.
- * A norm that is NaN or infinite (in fp32) clips nothing: `out` gets the gradients as they are, and the
- * caller sees the norm.  The sum is formed in fp64 in a fixed order.  Two launches for every
- * 120 tensors.
+ * The norm and the workspace must not overlap a tensor.  A norm that is NaN or infinite (in
+ * fp32) clips nothing: `out` gets the gradients as they are, and the caller sees the norm.
+ * The sum is formed in fp64 in a fixed order.  Two launches for every 120 tensors.
  */
 vim_status clip_grad_norm(const vim_tensor *tensors, int count, float max_norm, float *norm, void *workspace,
                           size_t workspace_bytes, cudaStream_t stream);

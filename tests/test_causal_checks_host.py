@@ -54,3 +54,18 @@ def test_gradients_and_their_outputs_are_paired(vs):
     for grads, out in ((dict(dD=a), [c]), ([a], dict(dD=c))):
         with pytest.raises(TypeError):
             pairs(grads, out)
+
+
+def test_norm_and_workspace_of_their_own(vs):
+    """The norm and the workspace are written while gradients are still read."""
+    need = vs.lib.clip_grad_norm_workspace_bytes(1)
+    def clip(table, norm=FAKE + (1 << 33), ws=FAKE + (1 << 34)):
+        return vs.lib.clip_grad_norm(i64(*table), len(table) // 4, 1.0, norm, ws, need, None)
+    in_place, apart = (FAKE, FAKE, 100, 0), (FAKE, FAKE + 4096, 100, 0)
+    for table in (in_place, apart):
+        for at in (FAKE, FAKE + 396):
+            assert clip(table, norm=at) == vs.VIM_ERR_INVALID_ARG
+        assert clip(table, ws=FAKE) == vs.VIM_ERR_INVALID_ARG
+        assert clip(table, ws=FAKE + 256) == vs.VIM_ERR_INVALID_ARG
+    assert clip(apart, norm=FAKE + 4096 + 200) == vs.VIM_ERR_INVALID_ARG
+    assert clip(in_place, norm=FAKE + (1 << 34) + need - 4) == vs.VIM_ERR_INVALID_ARG      # in the workspace

@@ -197,6 +197,20 @@ vim_status clip_impl(const vim_tensor *tensors, int count, float max_norm, float
     if (clip_overlap(tensors, count)) return VIM_ERR_INVALID_ARG;
     const int launches = clip_launches(count), parts = launches * kClipCtas;
     if (!workspace || workspace_bytes < clip_bytes(count) || misaligned(workspace, kAlign)) return VIM_ERR_WORKSPACE;
+    // the norm and the workspace are written while gradients are still to be read
+    auto meets = [](const void *a, uintptr_t na, const void *b, uintptr_t nb) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return x < y + nb && y < x + na;
+    };
+    const uintptr_t ws_bytes = clip_bytes(count);
+    if (meets(norm, sizeof(float), workspace, ws_bytes)) return VIM_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        const vim_tensor &t = tensors[i];
+        const uintptr_t bytes = (uintptr_t)t.n * elem_size((vim_dtype)t.dtype);
+        for (const void *at : {t.data, (const void *)t.out})
+            if (bytes && (meets(at, bytes, norm, sizeof(float)) || meets(at, bytes, workspace, ws_bytes)))
+                return VIM_ERR_INVALID_ARG;
+    }
     double *part = static_cast<double *>(workspace);
     auto table = [&](int launch, ClipTable &t) {
         std::memset(&t, 0, sizeof(t));
