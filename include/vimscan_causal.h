@@ -14,6 +14,9 @@
  *   - Tables on the device (offsets, slots) are not seen by the host checks.  The kernels
  *     bound them: no value leads to an access outside the tensors.
  *   - Inputs and outputs are aligned to their elements unless stated otherwise.
+ *   - An output must not overlap another tensor of the call except where it is said that it
+ *     may be an input.  Overlapping rows are refused where their strides are the same or
+ *     they start at the same address (VIM_ERR_INVALID_ARG); other overlaps are not seen.
  */
 #ifndef VIMSCAN_CAUSAL_H
 #define VIMSCAN_CAUSAL_H
@@ -129,7 +132,7 @@ size_t causal_bwd_workspace_bytes(int batch, int L, int d_inner, int d_state, in
  * over the past only):
  *   pre[b,t,c] = b[c] + sum_k w[c][k] x[b, t - width + 1 + k, c],   k = 0 .. width - 1
  *   y = silu(pre) where `silu` is non-zero, else pre
- *   x, y   : rows of `channels` (dt); y must not overlap x (the same address is refused).
+ *   x, y   : rows of `channels` (dt); y must not overlap x.
  *   w      : [channels, width] fp32, width 2, 3 or 4 (the newest tap last); b : [channels]
  *            fp32 or NULL.
  *   seqs   : states are [n_slots, width - 1, channels] (dt), aligned to their elements: the
@@ -142,7 +145,7 @@ typedef struct {
 vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, int batch, int L, int channels,
                        int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
 /* causal_conv for one token of each of `batch` sequences, rows as in causal_scan_step; state is
- * required, state_out NULL means in place. */
+ * required, state_out NULL means in place; y may be x itself. */
 vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *b, int batch, int channels,
                             int width, int silu, vim_dtype dt, const vim_sequences *seqs, cudaStream_t stream);
 /*

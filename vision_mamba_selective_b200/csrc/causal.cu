@@ -122,9 +122,14 @@ __global__ void __launch_bounds__(32 * kStepWarps) causal_step(const StepArgs p)
     }
 }
 
-bool bad_inputs(const vim_rows &u, const vim_rows &delta, const vim_rows &z, const vim_rows &B, const vim_rows &C,
-                vim_dtype dt) {
-    return bad_rows(u, dt) || bad_rows(delta, dt) || bad_rows(B, dt) || bad_rows(C, dt) || (z.data && bad_rows(z, dt));
+// the tensors of a call; y may be u, delta or z itself
+bool bad_tensors(const vim_rows &u, const vim_rows &delta, const vim_rows &z, const vim_rows &B, const vim_rows &C,
+                 const vim_rows &y, vim_dtype dt, int batch, int L, int d, int N) {
+    if (bad_rows(u, dt) || bad_rows(delta, dt) || bad_rows(B, dt) || bad_rows(C, dt) || (z.data && bad_rows(z, dt)) ||
+        bad_out(y, dt, batch, L, d))
+        return true;
+    return rows_clash(y, u, d, dt, batch, L) || rows_clash(y, delta, d, dt, batch, L) || rows_clash(y, z, d, dt, batch, L) ||
+           rows_meet(y, d, B, N, dt, batch, L) || rows_meet(y, d, C, N, dt, batch, L);
 }
 
 }  // namespace
@@ -149,12 +154,12 @@ vim_status causal_scan(const vim_scan_io *io, const float *A, const float *D, co
     if (!supported_state(d_state)) return VIM_ERR_UNSUPPORTED;
     CausalArgs a;
     std::memset(&a, 0, sizeof(a));
-    st = make_seqs(seqs, batch, L, 16, &a.seqs);
+    st = make_seqs(seqs, batch, L, 16, (int64_t)d_inner * d_state * sizeof(float), &a.seqs);
     if (st != VIM_OK) return st;
     if (ckpt && seqs && seqs->state) return VIM_ERR_INVALID_ARG;   // the derivative starts every sequence from zeros
     if (a.seqs.n == 0 || d_inner == 0) return VIM_OK;
     if (bad_params(A, D, delta_bias)) return VIM_ERR_INVALID_ARG;   // without tokens too: the kernel loads them first
-    if (L > 0 && (bad_inputs(u, delta, z, B, C, dt) || bad_out(y, dt, batch, L, d_inner) || misaligned(ckpt, 16)))
+    if (L > 0 && (bad_tensors(u, delta, z, B, C, y, dt, batch, L, d_inner, d_state) || misaligned(ckpt, 16)))
         return VIM_ERR_INVALID_ARG;
     a.u = u, a.delta = delta, a.z = z, a.B = B, a.C = C, a.y = y;
     a.A = A, a.D = D, a.bias = delta_bias;
@@ -180,11 +185,11 @@ vim_status causal_scan_step(const vim_scan_io *io, const float *A, const float *
     if (!rows.state_out) rows.state_out = const_cast<void *>(rows.state);
     StepArgs a;
     std::memset(&a, 0, sizeof(a));
-    st = make_seqs(&rows, batch, 1, 16, &a.seqs);
+    st = make_seqs(&rows, batch, 1, 16, (int64_t)d_inner * d_state * sizeof(float), &a.seqs);
     if (st != VIM_OK) return st;
     if (batch == 0 || d_inner == 0) return VIM_OK;
     if (!rows.state) return VIM_ERR_INVALID_ARG;
-    if (bad_params(A, D, delta_bias) || bad_inputs(u, delta, z, B, C, dt) || bad_out(y, dt, batch, 1, d_inner))
+    if (bad_params(A, D, delta_bias) || bad_tensors(u, delta, z, B, C, y, dt, batch, 1, d_inner, d_state))
         return VIM_ERR_INVALID_ARG;
     // the kernel's rows are the sequences
     vim_rows in[6] = {u, delta, z, B, C, y};

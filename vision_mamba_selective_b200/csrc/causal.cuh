@@ -4,7 +4,9 @@
 
 #include "vimscan_causal.h"
 
+#include <algorithm>
 #include <cstdint>
+#include <utility>
 
 #include "launch.cuh"
 
@@ -29,6 +31,35 @@ inline bool bad_out(const vim_rows &r, vim_dtype dt, int batch, int L, int width
     const bool tokens_inside = (L <= 1 || r.row_stride >= width) && (batch <= 1 || r.batch_stride >= rows);
     const bool items_inside = (batch <= 1 || r.batch_stride >= width) && (L <= 1 || r.row_stride >= items);
     return !tokens_inside && !items_inside;
+}
+// Whether two sets of rows, wa and wb elements wide, share elements: exactly where their strides are
+// the same, and by the first element where they are not.  Called with an output among the two, so
+// that equal strides are those of rows that do not overlap.
+inline bool rows_meet(const vim_rows &a, int wa, const vim_rows &b, int wb, vim_dtype dt, int batch, int L) {
+    if (!a.data || !b.data) return false;
+    if (a.data == b.data) return true;
+    if ((batch > 1 && a.batch_stride != b.batch_stride) || (L > 1 && a.row_stride != b.row_stride)) return false;
+    // element x of one is element y of the other where outer steps of s_out, inner steps of s_in
+    // and a difference of columns between -(wa - 1) and wb - 1 add up to `apart`
+    int64_t s_out = batch > 1 ? a.batch_stride : 0, s_in = L > 1 ? a.row_stride : 0, n_out = batch - 1, n_in = L - 1;
+    if (s_in > s_out) std::swap(s_in, s_out), std::swap(n_in, n_out);
+    const int64_t apart = (reinterpret_cast<intptr_t>(b.data) - reinterpret_cast<intptr_t>(a.data)) / (int64_t)elem_size(dt);
+    const int64_t reach = n_in * s_in + std::max(wa, wb);
+    const int64_t from = s_out ? std::max(-n_out, (apart - reach) / s_out - 1) : 0;
+    const int64_t to = s_out ? std::min(n_out, (apart + reach) / s_out + 1) : 0;
+    for (int64_t o = from; o <= to; ++o) {
+        const int64_t lo = apart - o * s_out - (wa - 1), hi = lo + wa + wb - 2;   // of the inner steps
+        int64_t i = 0;
+        if (s_in) i = std::min(n_in, std::max(-n_in, lo >= 0 ? (lo + s_in - 1) / s_in : -(-lo / s_in)));
+        if (i * s_in >= lo && i * s_in <= hi) return true;
+    }
+    return false;
+}
+// an output that may lie in the place of an input: the same rows or none of them
+inline bool rows_clash(const vim_rows &out, const vim_rows &in, int width, vim_dtype dt, int batch, int L) {
+    const bool same = out.data == in.data && (batch <= 1 || out.batch_stride == in.batch_stride) &&
+                      (L <= 1 || out.row_stride == in.row_stride);
+    return !same && rows_meet(out, width, in, width, dt, batch, L);
 }
 // the scan's parameters: A is read in vectors of four
 inline bool bad_params(const float *A, const float *D, const float *bias) {
@@ -56,8 +87,8 @@ struct Seqs {
     int n, L, n_slots;        // sequences, tokens per row, rows of the state cache
 };
 // Seqs of a call (v null: the batch rows, no states); `align` is what the states must be
-// aligned to
-inline vim_status make_seqs(const vim_sequences *v, int batch, int L, size_t align, Seqs *out) {
+// aligned to, `row_bytes` the size of a state row
+inline vim_status make_seqs(const vim_sequences *v, int batch, int L, size_t align, int64_t row_bytes, Seqs *out) {
     Seqs q = {nullptr, nullptr, nullptr, batch, L, 0};
     if (v) {
         if (v->n_seqs < 0 || v->n_slots < 0 || v->n_seqs > INT32_MAX || v->n_slots > INT32_MAX) return VIM_ERR_INVALID_ARG;
@@ -71,6 +102,10 @@ inline vim_status make_seqs(const vim_sequences *v, int batch, int L, size_t ali
         if (states && !v->slots && v->n_slots < v->n_seqs) return VIM_ERR_INVALID_ARG;
         if (misaligned(v->state, align) || misaligned(v->state_out, align) || misaligned(v->slots, 4))
             return VIM_ERR_INVALID_ARG;
+        if (v->state && v->state_out && v->state != v->state_out) {   // in place, or apart
+            const int64_t gap = reinterpret_cast<intptr_t>(v->state_out) - reinterpret_cast<intptr_t>(v->state);
+            if (row_bytes > 0 && (gap < 0 ? -gap : gap) / row_bytes < v->n_slots) return VIM_ERR_INVALID_ARG;
+        }
         q.cu = v->cu_seqlens;
         q.n = (int)v->n_seqs;
         q.slots = v->slots;

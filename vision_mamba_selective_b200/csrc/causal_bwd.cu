@@ -393,7 +393,7 @@ vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const floa
     seqs.n_seqs = cu_seqlens ? n_seqs : batch;
     CausalArgs pass;
     std::memset(&pass, 0, sizeof(pass));
-    st = make_seqs(&seqs, batch, L, 16, &pass.seqs);
+    st = make_seqs(&seqs, batch, L, 16, 0, &pass.seqs);
     if (st != VIM_OK) return st;
     if (d_inner == 0) return VIM_OK;
     if (!dA || !dD || !ddelta_bias || misaligned(dA, 4) || misaligned(dD, 4) || misaligned(ddelta_bias, 4))
@@ -410,11 +410,17 @@ vim_status causal_scan_bwd(const vim_scan_bwd_io *io, const float *A, const floa
         return VIM_ERR_INVALID_ARG;
     if (bad_params(A, D, delta_bias)) return VIM_ERR_INVALID_ARG;
     if (bad_out(du, dt, batch, L, d_inner) || bad_out(ddelta, dt, batch, L, d_inner)) return VIM_ERR_INVALID_ARG;
-    // (an output over an input: other warps may still have to read it)
-    for (const vim_rows *o : {&du, &ddelta, &dz})
-        for (const vim_rows *i : {&u, &delta, &z, &dout})
-            if (o->data && o->data == i->data) return VIM_ERR_INVALID_ARG;
     if (!z.data != !dz.data || (z.data && bad_out(dz, dt, batch, L, d_inner))) return VIM_ERR_INVALID_ARG;
+    // an output over an input (other warps may still have to read it), or over another output
+    const vim_rows *outs[] = {&du, &ddelta, &dz};
+    for (int k = 0; k < 3; ++k) {
+        for (const vim_rows *i : {&u, &delta, &z, &dout})
+            if (rows_meet(*outs[k], d_inner, *i, d_inner, dt, batch, L)) return VIM_ERR_INVALID_ARG;
+        for (const vim_rows *i : {&B, &C})
+            if (rows_meet(*outs[k], d_inner, *i, d_state, dt, batch, L)) return VIM_ERR_INVALID_ARG;
+        for (int j = 0; j < k; ++j)
+            if (rows_meet(*outs[k], d_inner, *outs[j], d_inner, dt, batch, L)) return VIM_ERR_INVALID_ARG;
+    }
     if (!dB || !dC || misaligned(dB, 4) || misaligned(dC, 4) || misaligned(ckpt, 16)) return VIM_ERR_INVALID_ARG;
     const CausalBwdPlan pl = causal_bwd_plan(batch, L, d_inner, d_state, ckpt != nullptr);
     if (pl.chunks > INT32_MAX || pl.slices > 65535) return VIM_ERR_UNSUPPORTED;

@@ -489,11 +489,12 @@ vim_status causal_conv(const vim_conv_io *io, const float *w, const float *b, in
     if (st != VIM_OK) return st;
     ConvArgs a;
     std::memset(&a, 0, sizeof(a));
-    st = make_seqs(seqs, batch, L, elem_size(dt), &a.seqs);
+    st = make_seqs(seqs, batch, L, elem_size(dt), (int64_t)(width - 1) * channels * elem_size(dt), &a.seqs);
     if (st != VIM_OK) return st;
     if (a.seqs.n == 0 || channels == 0) return VIM_OK;
     // (in place, tokens would be overwritten before their successors have read them)
-    if (L > 0 && (bad_rows(x, dt) || bad_out(y, dt, batch, L, channels) || y.data == x.data)) return VIM_ERR_INVALID_ARG;
+    if (L > 0 && (bad_rows(x, dt) || bad_out(y, dt, batch, L, channels) || rows_meet(y, channels, x, channels, dt, batch, L)))
+        return VIM_ERR_INVALID_ARG;
     a.x = x, a.y = y, a.w = w, a.b = b;
     a.state = seqs ? seqs->state : nullptr;
     a.state_out = seqs ? seqs->state_out : nullptr;
@@ -517,10 +518,11 @@ vim_status causal_conv_step(const vim_conv_io *io, const float *w, const float *
     if (!rows.state_out) rows.state_out = const_cast<void *>(rows.state);
     ConvArgs a;
     std::memset(&a, 0, sizeof(a));
-    st = make_seqs(&rows, batch, 1, elem_size(dt), &a.seqs);
+    st = make_seqs(&rows, batch, 1, elem_size(dt), (int64_t)(width - 1) * channels * elem_size(dt), &a.seqs);
     if (st != VIM_OK) return st;
     if (batch == 0 || channels == 0) return VIM_OK;
-    if (!rows.state || bad_rows(x, dt) || bad_out(y, dt, batch, 1, channels)) return VIM_ERR_INVALID_ARG;
+    if (!rows.state || bad_rows(x, dt) || bad_out(y, dt, batch, 1, channels) || rows_clash(y, x, channels, dt, batch, 1))
+        return VIM_ERR_INVALID_ARG;
     a.x = x, a.y = y, a.w = w, a.b = b;
     a.state = rows.state, a.state_out = rows.state_out;
     a.batch = batch, a.L = 1, a.d = channels, a.silu = silu != 0;
@@ -550,7 +552,7 @@ vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const floa
     seqs.n_seqs = cu_seqlens ? n_seqs : batch;
     ConvArgs a;
     std::memset(&a, 0, sizeof(a));
-    st = make_seqs(&seqs, batch, L, 16, &a.seqs);
+    st = make_seqs(&seqs, batch, L, 16, 0, &a.seqs);
     if (st != VIM_OK) return st;
     if (channels == 0) return VIM_OK;
     if (!dw || misaligned(dw, 4) || misaligned(db, 4) || (db && !b)) return VIM_ERR_INVALID_ARG;
@@ -560,8 +562,8 @@ vim_status causal_conv_bwd(const vim_conv_bwd_io *io, const float *w, const floa
                         (!db || cudaMemsetAsync(db, 0, n, stream) == cudaSuccess);
         return ok ? VIM_OK : VIM_ERR_CUDA;
     }
-    if (bad_rows(x, dt) || bad_rows(dout, dt) || bad_out(dx, dt, batch, L, channels) || dx.data == x.data ||
-        dx.data == dout.data)
+    if (bad_rows(x, dt) || bad_rows(dout, dt) || bad_out(dx, dt, batch, L, channels) ||
+        rows_meet(dx, channels, x, channels, dt, batch, L) || rows_meet(dx, channels, dout, channels, dt, batch, L))
         return VIM_ERR_INVALID_ARG;
     const size_t need = causal_conv_bwd_workspace_bytes(batch, L, channels, width);
     if (!workspace || workspace_bytes < need || misaligned(workspace, kAlign)) return VIM_ERR_WORKSPACE;
