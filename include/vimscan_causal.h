@@ -69,11 +69,13 @@ typedef struct {
  *   u, delta, z, y : rows of d_inner channels (dt); z.data may be NULL (no gate).  y may be
  *                    u, delta or z itself (the same rows); it must not overlap anything else.
  *   B, C           : rows of d_state (dt), shared by all channels of a token.
- *   A              : [d_inner, d_state] fp32, 16-byte aligned, meant to be <= 0 (of any
- *                    values; with A > 0 the decays of 16 tokens together must stay finite);
- *                    D, delta_bias : [d_inner] fp32.
+ *   A              : [d_inner, d_state] fp32, 16-byte aligned, meant to be <= 0, -infinity
+ *                    included (of any values; with A > 0 the decays of 16 tokens together
+ *                    must stay finite); D, delta_bias : [d_inner] fp32.
  *   seqs           : NULL: batch rows, no states.  States are fp32 [n_slots, d_inner,
- *                    d_state], 16-byte aligned.
+ *                    d_state], 16-byte aligned, and finite: one that is infinite, given or
+ *                    by an overflow, may become NaN where it would stay infinite token by
+ *                    token.
  *   ckpt           : NULL, or fp32 causal_ckpt_bytes(batch, L, d_inner, d_state) bytes,
  *                    16-byte aligned: the state entering every 8th token of a row,
  *                    [batch, ceil(L / 8), d_inner, d_state], for causal_scan_bwd; those

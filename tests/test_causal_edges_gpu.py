@@ -73,3 +73,37 @@ def test_norm_past_fp32_scales_nothing(vs, dtype):
     assert all(torch.equal(a, b) for a, b in zip(out, before))
     assert vs.clip_grad_norm(src, 1.0).item() == math.inf
     assert all(torch.equal(a, b) for a, b in zip(src, before))
+
+
+@pytest.mark.parametrize("batch,d,N,dtype", [(2, 40, 16, F32), (3, 264, 16, BF), (2, 600, 16, F32), (2, 4100, 16, F32),
+                                             (2, 24, 8, F32), (1, 20, 4, F32), (2, 20, 2, F32)])
+def test_a_at_minus_infinity(vs, batch, d, N, dtype):
+    """States that forget everything at once: A of -infinity, or of the type's lowest value, in
+    sequences whose ends lie inside a segment.  The definition has decays of exactly 0 there."""
+    L = 21
+    p = inputs((batch, L), d, N, dtype, seed=d)
+    p["A"][1, 1], p["A"][3], p["A"][d - 1, 0] = -math.inf, -math.inf, torch.finfo(F32).min
+    state = torch.empty((batch, d, N), device="cuda")
+    ck = torch.full(vs.causal_ckpt_shape(batch, L, d, N), float("nan"), device="cuda")
+    args = cuda(p)
+    y = vs.causal_scan(*args, state_out=state, ckpt=ck)
+    want, last = causal_ref.scan(p["u"], p["delta"], p["z"], p["B"], p["C"], p["A"], p["D"], p["bias"])
+    close(y, want, Y_TOL[dtype], "y")
+    close(state, last, STATE_TOL, "state")
+    assert torch.isfinite(ck).all()
+    token = [t[:, 3] for t in args[:5]]
+    start = torch.randn((batch, d, N), generator=torch.Generator().manual_seed(2))
+    got = start.cuda()
+    vs.causal_scan_step(*token, *args[5:], got)
+    one = {k: (v[:, 3:4] if k in ("u", "delta", "z", "B", "C") else v) for k, v in p.items()}
+    close(got, causal_ref.scan(one["u"], one["delta"], one["z"], one["B"], one["C"], p["A"], p["D"], p["bias"],
+                               starts=start)[1], STATE_TOL, "step")
+    # the derivative: what -1e30, whose decays are 0 as well, gives (its slope with respect to A is 0)
+    dout = torch.randn((batch, L, d), generator=torch.Generator().manual_seed(3)).to(dtype).cuda()
+    near = list(args)
+    near[5] = args[5].clamp(min=-1e30)
+    for kept in (None, ck):
+        g, w = vs.causal_scan_bwd(*args, dout, ckpt=kept), vs.causal_scan_bwd(*near, dout, ckpt=kept)
+        for k in g:
+            assert torch.equal(g[k], w[k]), k
+        assert (g["dA"][3] == 0).all()

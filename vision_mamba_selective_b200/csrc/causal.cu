@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) causal_step(const StepArgs p)
     const float bias = p.bias[c], Dc = p.D[c];
     float A[NL];
 #pragma unroll
-    for (int i = 0; i < NL; ++i) A[i] = p.A[(int64_t)c * N + q * NL + i] * kLog2e;
+    for (int i = 0; i < NL; ++i) A[i] = decay_rate(p.A[(int64_t)c * N + q * NL + i]);
     const int mine = c * N + q * NL, row = p.d * N;        // the lane's states in a slot's row
 
     float h[R][NL];

@@ -5,6 +5,7 @@
 #include "vimscan_causal.h"
 
 #include <algorithm>
+#include <cfloat>
 #include <cstdint>
 #include <utility>
 
@@ -209,6 +210,10 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 // 10^6 arguments per octave; a step of 0 still gives exactly 1), and the addition is part
 // of the multiplication that forms the argument.
 constexpr float kDecayShift = 2.0e-8f;
+// A log2(e).  Held finite, so that a step of 0 (tokens outside a sequence) leaves the state as it is
+// where A is -infinity; every step above 1e-36 then still gives a decay of 0.
+__device__ __forceinline__ float decay_rate(float A) { return max_nan(A * kLog2e, -FLT_MAX); }
+__device__ __forceinline__ float2 decay_rate(float2 A) { return f2(decay_rate(A.x), decay_rate(A.y)); }
 __device__ __forceinline__ float decay(float A2, float dt) { return ex2(fmaf(A2, dt, kDecayShift)); }
 __device__ __forceinline__ float2 decay(float2 A2, float dt) {
     const float2 e = fma2(A2, f2(dt, dt), f2(kDecayShift, kDecayShift));

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const Causa
         load_row<NP>(p.A + (int64_t)c * N + q * NL, A2);
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            A2[i] = mul2(A2[i], f2(kLog2e, kLog2e));
+            A2[i] = decay_rate(A2[i]);
             dA[i] = g[i] = f2(0.0f, 0.0f);
         }
         const float bias = p.bias[c], Dc = p.D[c];

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
     float2 A2[NP];
     load_row<NP>(p.A + (int64_t)c * N + q * NL, A2);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) A2[i] = mul2(A2[i], f2(kLog2e, kLog2e));
+    for (int i = 0; i < NP; ++i) A2[i] = decay_rate(A2[i]);
     const float bias = p.bias[c], Dc = MODE == kForward ? p.D[c] : 0.0f;
 
     // segments of the sequence; m = 0 is the first in the order of the walk
