@@ -29,12 +29,13 @@ vim_status launch_pass_t(const CausalArgs &a, int N, cudaStream_t stream) {
         case 4: return launch_pass_v<T, 4, 2, 8, MODE>(a, pl.warps, stream);
         case 8: return launch_pass_v<T, 8, 4, 8, MODE>(a, pl.warps, stream);
         default:
-            if constexpr (MODE != kStates) {
-                if (MODE == kForward && pl.states == 2) return launch_pass_v<T, 16, 2, kLongSeg, MODE>(a, pl.warps, stream);
+            if (pl.states == 8) return launch_pass_v<T, 16, 8, 4, MODE>(a, pl.warps, stream);
+            if constexpr (MODE == kForward) {
+                if (pl.states == 2) return launch_pass_v<T, 16, 2, kLongSeg, MODE>(a, pl.warps, stream);
                 if (pl.seg == kLongSeg) return launch_pass_v<T, 16, 4, kLongSeg, MODE>(a, pl.warps, stream);
             }
-            return pl.states == 8 ? launch_pass_v<T, 16, 8, 4, MODE>(a, pl.warps, stream)
-                                  : launch_pass_v<T, 16, 4, kSeg, MODE>(a, pl.warps, stream);
+            // (the adjoint, which has no other plan here, always in long segments)
+            return launch_pass_v<T, 16, 4, MODE == kAdjoint ? kLongSeg : kSeg, MODE>(a, pl.warps, stream);
     }
 }
 
