@@ -19,7 +19,7 @@ namespace {
 // computed (without that the chain slot -> state -> store leaves memory idle half of the
 // time).  Each of a channel's lanes forms Delta and the gate of one of the LPC sequences,
 // exchanged by shuffles, so that no lane repeats another's work.  256 x 4096, N = 16, bf16:
-// 27 us on the device, 22 at the copy rate for the 143 MB.
+// 28 us on the device, 22 at the copy rate for the 143 MB.
 struct StepArgs {
     vim_rows u, delta, z, B, C, y;         // row b: sequence b
     const float *A, *D, *bias;

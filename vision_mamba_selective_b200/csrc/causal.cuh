@@ -197,6 +197,8 @@ __device__ __forceinline__ float softplus_slope(float x, float &slope) {
     return softplus_acc(x);
 }
 
+// 1 / (1 + exp(-x)).  The rounding of x log2(e) is not carried along: up to 7e-7 relative at |x| near
+// 20, in an output or gradient that is not added up over tokens
 __device__ __forceinline__ float sigmoid(float x) { return rcp(1.0f + ex2(-x * kLog2e)); }
 
 template <typename T> __device__ __forceinline__ T from_f32(float x);

@@ -8,6 +8,9 @@
 //   dA = sum_t g m Delta       dD = sum_t dy u               dbias = sum_t ddelta
 //   dz = dout (C . h + D u) silu'(z)
 //
+// The sums are fp32: over at most 64 tokens (dA, dD, dbias) or a CTA's channels (dB, dC) in one
+// thread or warp, then over the chunks or slices by 16 partial sums or in a row.
+//
 // Launches: the states every 8 tokens, unless the caller kept them; the adjoint carries
 // entering every 64 tokens (both causal_pass); the kernel below over 64-token chunks,
 // all independent of one another; the sums over what its CTAs left.  Every sum is taken
@@ -53,9 +56,10 @@ __device__ __forceinline__ float reduce_channels(float (&v)[n], int cl) {
 // Bound by latency and issue: 960 instructions per 64 token-channels, 192 of them the packed
 // arithmetic, 250 the selects and shuffles of the sums (dB and dC over channels, three
 // sums over states), at half an instruction a clock and scheduler.  Two CTAs an SM, with
-// room for all of a segment in registers: at three the compiler spills 250 bytes a thread
-// (8 x 4097 tokens x 384 channels, N = 16, bf16: 320 us, 510 with the spills; with m_t in
-// shared memory and loads held back, so that three fit, 330).
+// room for a segment in registers (at N = 8, whose 16 channels a warp take longer sums, 12 to
+// 32 bytes a thread spill all the same): at three the compiler spills 250 bytes a thread (8 x
+// 4097 tokens x 384 channels, N = 16, bf16: 308 us; taken at 320 against 510 with the spills, and
+// against 330 with m_t in shared memory and loads held back, so that three fit).
 template <typename T, int N, int NL, bool PACKED>
 __global__ void __launch_bounds__(32 * kBwdWarps, 2) causal_bwd_main(const CausalBwdArgs p) {
     constexpr int LPC = N / NL, CH = 32 / LPC, NP = NL / 2, EPL = kSeg / LPC, NV = 2 * NL;

@@ -35,11 +35,11 @@
 // The adjoint, and the states kept for the derivative, are wanted only at segment borders:
 // these modes end with step 3, and wait mostly for the handovers (200 to 250 clocks each).  The
 // adjoint, which keeps nothing per token, therefore takes segments of 16 (8 x 4097 tokens x
-// 384 channels: 95 us, 105 with 8).
+// 384 channels: 90 us; taken at 95 against 105 with 8).
 //
 // Measured at N = 16, bf16 (the special-function floor in parentheses): 8192 packed tokens x
-// 2048 channels 145 us (74), 4 x 16385 x 384 342 us (111), 8 x 4097 x 384 with kept states
-// 141 us (55), 1 x 16385 x 384 139 us (28); 0.65 instructions a clock and scheduler, shared-memory pipe at 67%.
+// 2048 channels 140 us (74), 4 x 16385 x 384 326 us (111), 8 x 4097 x 384 with kept states
+// 137 us (55), 1 x 16385 x 384 139 us (28); 0.64 instructions a clock and scheduler, shared-memory pipe at 68%.
 #pragma once
 
 #include "causal.cuh"
@@ -126,9 +126,10 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
     int s = blockIdx.x / blocks;
     if (p.seqs.cu && p.seqs.n > 1 && p.seqs.n <= kMostRanked) {
         // packed sequences from the longest to the shortest, so that no long one starts last
-        // (8192 tokens x 2048 channels in 11 and 60 sequences, mean of 8 draws: 166 -> 147 and
-        // 202 -> 175 us): CTA group k takes the sequence that k others are longer than (or as
-        // long, and before)
+        // (8192 tokens x 2048 channels, mean of 8 draws, without and with it: in 11 sequences 165
+        // and 146 us, in 60 203 and 174, in 64 180 and 175): CTA group k takes the sequence that k
+        // others are longer than (or as long, and before).  Every CTA counts for itself, which
+        // past kMostRanked costs more than the order gives (in 96 187 and 202, in 128 183 and 250)
         int *const found = reinterpret_cast<int *>(pass_smem);
         for (int i = threadIdx.x; i < p.seqs.n; i += blockDim.x) {
             const int length = p.seqs.cu[i + 1] - p.seqs.cu[i];
@@ -340,23 +341,24 @@ inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 //   - Eight states and segments of 4 (16 channels a warp, 32-byte rows at bf16) need fewer
 //     loads, shuffles and selects per token-channel than four and segments of 8, but half
 //     the CTAs and twice the handovers per token: better from 8192 channels on (4 x 2048
-//     tokens x 4096: 279 us against 301), worse below (1 x 4096 tokens x 2048 channels: 113
-//     and 92).  Packed, where one sequence may hold most of the tokens, from 16384 on (8192
-//     tokens in 11 sequences x 2048 channels: 147 and 168; in 4: 227 and 164; 4000 tokens in
-//     20 x 768: 45 and 38).
+//     tokens x 4096: 274 us against 291), worse below (1 x 4096 tokens x 2048 channels: 113
+//     and 88).  Packed, where one sequence may hold most of the tokens, from 16384 on (8192
+//     tokens in 11 sequences x 2048 channels: 146 and 160; in 4: 174 and 156; 4000 tokens in
+//     20 x 768: 52 and 40).
 //   - Where four states a lane give no SM a second CTA, up to 1184 channels, the forward mode
 //     may use all registers, for segments of 16 and half the handovers (2 x 16385 tokens x 384
-//     channels: 176 us against 244; 1 x 4096 x 1184: 49 and 67); and with two states a lane, half
-//     as many instructions again but twice the CTAs, up to 592 (1 x 16385 x 384: 139 us, 244 in
-//     segments of 8; 1 x 4096 x 592: 41 and 67).  Past 592 the latter loses (4 x 16385 x 384:
-//     459 us against 342), past 1184 the former too (8 x 197 x 192: 14.3 and 12.3; 1 x 4096 x
-//     1600: 98 and 94; only 4 x 16385 x 384 gains, 336 and 342).
-//   - Eight warps hide the handover best; four waste less where sequences are short
-//     (64 x 16 tokens x 4096 channels: 68 us against 115; 16 x 200 x 2048: 61 and 68; 64 x
-//     500 x 768: 203 and 209; 11 packed sequences of 745 tokens on average: 162 and 147),
-//     and where the CTAs then run in one wave instead of a full and a partial one (8 x 4097
-//     tokens x 384 channels: 141 and 151).  A row has no work for more warps than
-//     segments.
+//     channels: 174 us against 223; 1 x 4096 x 1184: 49 and 61); and with two states a lane, half
+//     as many instructions again but twice the CTAs, up to 592 (1 x 16385 x 384: 139 us, 170 with
+//     four, 217 in segments of 8; 1 x 4096 x 592: 41, 49 and 59).  Past 592 the latter loses (2 x
+//     16385 x 384: 266 us against 174), past 1184 the former too (1 x 4096 x 1600: 96 and 90; 4 x
+//     16385 x 384: 332 and 328).
+//   - Eight warps hide the handover best (11 packed sequences of 745 tokens on average: 146 us,
+//     169 with four); four waste less where sequences are short (200 x 30 tokens x 384
+//     channels: 31 us against 45; 64 x 100 x 768: 47 and 55; 16 x 200 x 2048: 58 and 63; still
+//     123 and 130 for 64 x 300 x 768).  Where the CTAs then run in one wave instead of a full
+//     and a partial one four are taken too; the two are within a few per cent there (8 x 4097 x
+//     384: 134 and 132 us at bf16, 134 and 138 at fp32; 4 x 300 x 1100: 16.9 and 17.9), but 2 x
+//     4000 x 2048, 172 and 161.  A row has no work for more warps than segments.
 struct PassPlan {
     int states, seg, warps;
 };

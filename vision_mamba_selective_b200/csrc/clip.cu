@@ -11,7 +11,7 @@
 // relative error of a few 2^-24) and in fp64 from there on; the CTAs' sums are added in a
 // fixed order, by every CTA of the scaling launch for itself, which saves a launch between
 // the two.  The scaling walks the units backwards: what the norm read last is still in L2.
-// 320 M elements (60 tensors bf16 and fp32): 315 us for 1.9 GB, 6.1 TB/s; 37 small tensors: 12 us.
+// 320 M elements (60 tensors bf16 and fp32): 315 us for 1.9 GB, 6.1 TB/s; 37 small tensors: 11 us.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -7,8 +7,10 @@
 // down the tokens of four neighbouring channels with the last W - 1 inputs in registers: each
 // input is read once, a turn of 8 (4) tokens ahead.  At bf16 the SiLU is then as long as the
 // traffic: two special-function operations an element, 7.5 us for 8192 x 2048 (10.3 us of
-// traffic, 20.5 us measured, by latency: 14 warps an SM; strips of 8 channels, twice the
-// warps with shorter runs: 22 to 26 us).  8 x 4097 x 384: 16 us forward, 29 us backward.
+// traffic).  Measured 21 us: 0.47 instructions a clock and scheduler at 14 warps an SM, which wait
+// for fixed latencies first and for loads second, too few of them to cover either (strips of 8
+// channels, or twice the warps with shorter runs: 22 to 26 us); 29 us at fp32 (20.6 of traffic).
+// 8 x 4097 x 384, bf16: 16 us forward, 27 us backward.
 #include "causal.cuh"
 
 #include <algorithm>
@@ -273,7 +275,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_step(const ConvArgs p) {
 // Derivative for sequences that start from zeros.  With dpre_t = dout_t silu'(pre_t):
 //   dx_t = sum_j w_(W-1-j) dpre_(t + j),  dw_k = sum_t dpre_t x_(t - W + 1 + k),  db = sum_t dpre_t
 // A thread forms dpre along its run and W - 1 tokens past it (so that its dx are complete);
-// dw and db take the run's own tokens.  The runs' sums go to `part`.
+// dw and db take the run's own tokens, in fp32.  The runs' sums go to `part`.  Four CTAs an SM
+// leave 128 registers, in which the inputs loaded ahead do not all fit at fp32 (width 4: 188
+// bytes spilled, width 3: 56; at bf16 none but 4) nor without whole vectors (up to 224).
+// Forward and derivative at 8 x 4097 x 384: bf16 47 us (19 of traffic), fp32 77 us (38).
 template <typename T, int W, int V, bool VEC>
 __global__ void __launch_bounds__(kConvThreads, 4) conv_bwd(const ConvArgs p) {
     const ConvSpot o = conv_spot<V>(p);

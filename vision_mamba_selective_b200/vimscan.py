@@ -4,7 +4,8 @@ operators, include/vimscan_causal.h).
 Argument marshalling only: every tensor is checked for device (the current CUDA
 device), dtype, shape and contiguity before the library is called, then turned into
 raw device pointers and handed to the C ABI together with
-the current torch CUDA stream.  Every step of the scan runs in the library's sm_100a
+the current torch CUDA stream, or ``stream=``, which is then the current one for the whole of
+the call.  Every step of the scan runs in the library's sm_100a
 kernels; there is no fallback of any kind, and a missing library is an ImportError.
 """
 from __future__ import annotations
@@ -921,7 +922,8 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
 
     ``ckpt``, fp32 of causal_ckpt_shape(...), receives the states causal_scan_bwd takes (not
     together with ``state``: the derivative starts every sequence from zeros).
-    Returns y, shaped like u.
+    Returns y, shaped like u.  Tokens of no sequence and of padding entries keep what y held;
+    where y is allocated here that is not initialised.
     """
     where = "causal_scan"
     if ckpt is not None and state is not None:
@@ -952,8 +954,8 @@ def causal_scan(u, delta, z, B, C, A, D, delta_bias, *, cu_seqlens=None, state=N
 def causal_scan_step(u, delta, z, B, C, A, D, delta_bias, state, *, state_out=None, slots=None, y=None, stream=None):
     """causal_scan for one token of each sequence: u, delta, z [batch, d_inner], B, C
     [batch, d_state], state as there (required; updated in place unless ``state_out`` is
-    given).  Rows whose slot is outside the cache are padding: their y is left as it was.
-    Returns y [batch, d_inner].
+    given).  Rows whose slot is outside the cache are padding: their y is left as it was (not
+    initialised where y is allocated here).  Returns y [batch, d_inner].
     """
     where = "causal_scan_step"
     dev = _check_ref(where, u)
@@ -1045,7 +1047,8 @@ def causal_conv(x, w, b, *, silu=True, cu_seqlens=None, state=None, state_out=No
     x: [batch, L, channels], or [tokens, channels] with ``cu_seqlens``, any row strides.  w:
     [channels, width] fp32, width 2 to 4, the newest tap last; b: [channels] fp32 or None.
     state: [rows, width - 1, channels] in x's dtype, the last inputs of each sequence, oldest
-    first; state_out, slots and fresh as in causal_scan.  Returns y, shaped like x.
+    first; state_out, slots and fresh as in causal_scan.  Returns y, shaped like x; tokens of no
+    sequence as in causal_scan.
     """
     where = "causal_conv"
     dev = _check_ref(where, x)
