@@ -104,3 +104,17 @@ def test_stream_inside_a_capture(vs):
             torch.cuda.synchronize()
             for x, y in zip(values(got), want):
                 assert torch.equal(x, y), name
+
+
+def test_given_outputs(vs):
+    """Outputs and workspace of the caller's, on another stream; what else their dict holds stays."""
+    a = cuda(inputs((2, 130), 40, 16, F32, 3))
+    dout = torch.ones((2, 130, 40), device="cuda")
+    want = vs.causal_scan_bwd(*a, dout)
+    out = {k: torch.full_like(v, 7.0) for k, v in want.items()} | {"name": "block 1"}
+    ws = torch.empty(vs.causal_bwd_workspace_bytes(2, 130, 40, 16, False), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert vs.causal_scan_bwd(*a, dout, out=out, workspace=ws, stream=side) is out
+    torch.cuda.current_stream().wait_stream(side)
+    assert out.pop("name") == "block 1" and all(torch.equal(out[k], want[k]) for k in want)

@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(32 * kPassWarps, pass_ctas(MODE, SEG)) causal_
 // states of B (C) that a lane fetches of a segment
 inline int lane_states(int N) { return N >= 4 ? N / 4 : 1; }
 
-// How a call is cut: states a lane holds, tokens of a segment, warps of a CTA.
+// How a call is cut: states a lane holds, tokens of a segment, warps of a CTA.  (Figures at N = 16
+// and bf16 unless said otherwise.)
 //   - Eight states and segments of 4 (16 channels a warp, 32-byte rows at bf16) need fewer
 //     loads, shuffles and selects per token-channel than four and segments of 8, but half
 //     the CTAs and twice the handovers per token: better from 8192 channels on (4 x 2048

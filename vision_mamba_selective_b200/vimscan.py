@@ -235,7 +235,7 @@ def _on_stream(entry):
         with torch.cuda.stream(stream):
             result = entry(*args, **kw)
         for t in result.values() if isinstance(result, dict) else (result,):
-            if t is not None and t.is_cuda:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
                 t.record_stream(caller)
         return result
     return call
